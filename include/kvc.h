@@ -400,6 +400,154 @@ kvc_status kvc_plan_stream(const uint64_t *chunk_bytes, uint32_t n_chunks, uint3
                            const kvc_bw_piece *trace, uint32_t n_pieces, double slo_s,
                            double init_bytes_per_s, uint8_t *levels_out, double *finish_s_out);
 
+/* ------------------------------------------------------------ paged KV cache */
+/*
+ * Serving over a restored cache: new tokens written into it (kvc_append),
+ * attention of new tokens over it (kvc_attend for one new token a sequence,
+ * kvc_attend_prompt for several), and a context's tokens moved between pages
+ * and a tensor of their own (kvc_page_out, kvc_page_in).
+ *
+ * The pool is a KV cache in the layout of every other call,
+ * [L][2][n_pages * page_tokens][C] with C = n_kv_heads * head_dim: page p is
+ * the token rows [p * page_tokens, (p + 1) * page_tokens).  kvc_decode,
+ * kvc_decode_multi and kvc_restore therefore write straight into a pool
+ * (T_total = n_pages * page_tokens) wherever a chunk's tokens lie in
+ * consecutive pages; kvc_page_in scatters a decoded tensor otherwise, and
+ * kvc_page_out gathers what kvc_encode reads.
+ *
+ * Types: cache_dtype is the pool's element type, io_dtype that of q, k, v and
+ * out; they are equal, or io_dtype is KVC_BF16 over a KVC_F16 pool (a
+ * bfloat16 model on the codec's binary16 cache).  In that pair k and v are
+ * rounded to binary16 when they are written (beyond +-65504: infinity) and q
+ * when it is used (exact between 2^-14 and 65504 in magnitude).
+ *
+ * Device errors differ from the other calls' in one point: these calls do
+ * NOT set *dev_status to 0 first, so that a step of many layers costs no
+ * extra launches and is checked once; the caller zeroes the word and reads
+ * it when it likes.  A page id outside the pool, a length above max_len, a
+ * position the rotation table does not hold or a q_start that decreases or
+ * passes n_tokens stores KVC_ERR_SHAPE (the first error stays); nothing out
+ * of bounds is read or written, and only the outputs are unspecified.
+ */
+typedef enum { KVC_F16 = 0, KVC_BF16 = 1 } kvc_dtype;
+
+typedef struct {
+  uint32_t n_layers;    /* 1 .. 32767 */
+  uint32_t n_heads;     /* query heads, at most 4096: a multiple of n_kv_heads, at most
+                           128 for each */
+  uint32_t n_kv_heads;  /* >= 1 */
+  uint32_t head_dim;    /* 64, 96, 128 or 256 */
+  uint32_t page_tokens; /* >= 1 */
+  uint32_t n_pages;     /* >= 1; n_pages * page_tokens < 2^31 */
+  uint32_t cache_dtype; /* kvc_dtype */
+  uint32_t io_dtype;    /* kvc_dtype */
+} kvc_paged_desc;
+
+/*
+ * A batch of sequences.  Sequence b's token t is in page table[b][t /
+ * page_tokens]; entries its length does not reach are never read.  lens[b]
+ * counts its tokens in the cache, the new ones included; its new tokens are
+ * rows [q_start[b], q_start[b+1]) of q, k, v and out, the last ones of the
+ * sequence: row q_start[b] + i has position lens[b] - n_b + i.  A row whose
+ * position is negative is padding (an unused slot of a captured batch:
+ * lens[b] = 0): kvc_append skips it, attention gives it zeros.  Rows from
+ * q_start[n_seqs] on are neither read nor written.
+ */
+typedef struct {
+  const int32_t *table;   /* device [n_seqs][table_stride] page ids */
+  const int32_t *lens;    /* device [n_seqs] */
+  const int32_t *q_start; /* device [n_seqs + 1], or NULL: one new token each */
+  uint32_t n_seqs;        /* at most 2^20 */
+  uint32_t table_stride;  /* entries in a row of table */
+  uint32_t n_tokens;      /* rows of q, k, v, out, at most 2^20; n_seqs if q_start is NULL */
+  uint32_t max_len;       /* bound of lens, at most table_stride * page_tokens */
+} kvc_paged_batch;
+
+/*
+ * Rotation of keys and queries: cos_sin holds for every position
+ * rotary_dim / 2 cosines, then as many sines.  The first rotary_dim
+ * dimensions of a head are turned in pairs (a, b) -> (a cos - b sin,
+ * b cos + a sin): dimensions (j, j + rotary_dim / 2), or (2j, 2j + 1) if
+ * interleaved; the others are left as they are.
+ */
+typedef struct {
+  const float *cos_sin; /* device [n_positions][rotary_dim], 16-byte aligned */
+  uint32_t n_positions;
+  uint32_t rotary_dim;  /* a multiple of 16, at most head_dim */
+  uint32_t interleaved; /* 0 or 1 */
+  uint32_t reserved;    /* 0 */
+} kvc_rope;
+
+/* KVC_OK if the descriptor is supported, else KVC_ERR_INVALID_ARG. */
+kvc_status kvc_validate_paged_desc(const kvc_paged_desc *p);
+
+/*
+ * Write the batch's new tokens into layer `layer` of `pool`: keys turned to
+ * their positions (rope NULL: as they are), values as they are; and the
+ * queries, if q is not NULL, turned the same way into q_out (which may be q
+ * itself, with the same stride).  k, v: [n_tokens][n_kv_heads][head_dim],
+ * q, q_out: [n_tokens][n_heads][head_dim]; *_stride: elements from one token
+ * to the next, so that slices of one projection's rows can be passed.
+ * Pointers are 16-byte aligned and strides multiples of 8 (else
+ * KVC_ERR_INVALID_ARG).  Tokens of one call must go to different slots.
+ */
+kvc_status kvc_append(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t layer,
+                      void *pool, const void *k, uint64_t k_stride, const void *v,
+                      uint64_t v_stride, const void *q, uint64_t q_stride, void *q_out,
+                      uint64_t q_out_stride, const kvc_rope *rope, int32_t *dev_status,
+                      hipStream_t stream);
+
+/* Workspace bytes of kvc_attend and kvc_attend_prompt for a batch of these
+ * sizes (n_seqs, n_tokens, max_len are read, and whether q_start is NULL).
+ * 0 if the descriptor or the batch is invalid. */
+uint64_t kvc_attend_ws_bytes(const kvc_paged_desc *p, const kvc_paged_batch *b);
+
+/*
+ * Attention of one new token per sequence (q_start NULL) over layer `layer`
+ * of the pool: query head h reads KV head h / (n_heads / n_kv_heads);
+ *   s_j = scale * q.k_j over the visible tokens j <= position, and
+ *   j > position - window if window > 0;
+ *   out = sum_j exp(s_j - lse) v_j,  lse = log sum_j exp(s_j).
+ * A row without a visible token gives zeros and lse = -infinity; what lies
+ * in hidden tokens (infinities and NaN included) has no effect.  out:
+ * [n_tokens][n_heads][head_dim] with out_stride elements from one token to
+ * the next; lse: [n_tokens][n_heads] binary32, or NULL.  The new tokens' own
+ * keys and values are read from the pool (kvc_append first).
+ */
+kvc_status kvc_attend(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t layer,
+                      const void *pool, const void *q, uint64_t q_stride, float scale,
+                      uint32_t window, void *out, uint64_t out_stride, float *lse, void *ws,
+                      uint64_t ws_bytes, int32_t *dev_status, hipStream_t stream);
+
+/* The same with q_start: several new tokens per sequence, each seeing the
+ * tokens up to its own position. */
+kvc_status kvc_attend_prompt(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t layer,
+                             const void *pool, const void *q, uint64_t q_stride, float scale,
+                             uint32_t window, void *out, uint64_t out_stride, float *lse,
+                             void *ws, uint64_t ws_bytes, int32_t *dev_status,
+                             hipStream_t stream);
+
+/*
+ * Copy tokens [first_token, first_token + n_tokens) of one sequence, every
+ * layer, from its pages (table: device [table_entries]) to the token rows
+ * [out_first, out_first + n_tokens) of kv_out [L][2][T_total][C], bit for
+ * bit.  Needs first_token + n_tokens <= table_entries * page_tokens and
+ * n_tokens <= 2^27.
+ * kv_out and the pool must not overlap.
+ */
+kvc_status kvc_page_out(const kvc_paged_desc *p, const void *pool, const int32_t *table,
+                        uint32_t table_entries, uint32_t first_token, uint32_t n_tokens,
+                        void *kv_out, uint32_t T_total, uint32_t out_first, int32_t *dev_status,
+                        hipStream_t stream);
+
+/* The way back: token rows [in_first, in_first + n_tokens) of kv_in
+ * [L][2][T_total][C] into the pages.  Rows of the pages outside the token
+ * range are left as they are; no page may stand twice in the range. */
+kvc_status kvc_page_in(const kvc_paged_desc *p, const void *kv_in, uint32_t T_total,
+                       uint32_t in_first, void *pool, const int32_t *table,
+                       uint32_t table_entries, uint32_t first_token, uint32_t n_tokens,
+                       int32_t *dev_status, hipStream_t stream);
+
 /*
  * Debug form of kvc_decode: same kernels, but writes the decoded symbols
  * (u8: anchor 0..255, delta q + M) to sym_out [L][2][T_total][C] instead of

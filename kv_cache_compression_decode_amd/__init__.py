@@ -41,6 +41,8 @@ EXPORTED = (
     "kvc_plan_stream", "kvc_decode_multi", "kvc_decode_static", "kvc_refine_tables_bytes",
     "kvc_refine_profile_ws_bytes", "kvc_profile_refine", "kvc_encode_refine_ws_bytes",
     "kvc_encode_refine", "kvc_decode_refined_ws_bytes", "kvc_decode_refined",
+    "kvc_validate_paged_desc", "kvc_append", "kvc_attend_ws_bytes", "kvc_attend",
+    "kvc_attend_prompt", "kvc_page_out", "kvc_page_in",
 )
 
 
@@ -123,6 +125,50 @@ class HostChunk(ctypes.Structure):
     ]
 
 
+class PagedDesc(ctypes.Structure):
+    """kvc_paged_desc: a KV cache whose token axis is cut into pages, and the
+    model that reads it."""
+    _fields_ = [
+        ("n_layers", ctypes.c_uint32),
+        ("n_heads", ctypes.c_uint32),
+        ("n_kv_heads", ctypes.c_uint32),
+        ("head_dim", ctypes.c_uint32),
+        ("page_tokens", ctypes.c_uint32),
+        ("n_pages", ctypes.c_uint32),
+        ("cache_dtype", ctypes.c_uint32),
+        ("io_dtype", ctypes.c_uint32),
+    ]
+
+    @property
+    def pool_shape(self) -> Tuple[int, int, int, int]:
+        return (self.n_layers, 2, self.n_pages * self.page_tokens,
+                self.n_kv_heads * self.head_dim)
+
+
+class _PagedBatch(ctypes.Structure):
+    """kvc_paged_batch."""
+    _fields_ = [
+        ("table", ctypes.c_void_p),
+        ("lens", ctypes.c_void_p),
+        ("q_start", ctypes.c_void_p),
+        ("n_seqs", ctypes.c_uint32),
+        ("table_stride", ctypes.c_uint32),
+        ("n_tokens", ctypes.c_uint32),
+        ("max_len", ctypes.c_uint32),
+    ]
+
+
+class _RopeArgs(ctypes.Structure):
+    """kvc_rope."""
+    _fields_ = [
+        ("cos_sin", ctypes.c_void_p),
+        ("n_positions", ctypes.c_uint32),
+        ("rotary_dim", ctypes.c_uint32),
+        ("interleaved", ctypes.c_uint32),
+        ("reserved", ctypes.c_uint32),
+    ]
+
+
 def make_desc(n_layers: int, n_channels: int,
               delta_bits: Sequence[Sequence[int]] = ((6, 5, 4),),
               group_tokens: int = 10, chunk_tokens: int = 1500) -> CodecDesc:
@@ -198,6 +244,22 @@ def lib():
     L.kvc_decode_refined.restype = ctypes.c_int
     L.kvc_plan_stream.argtypes = [vp, u32, u32, vp, u32, ctypes.c_double, ctypes.c_double, vp, vp]
     L.kvc_plan_stream.restype = ctypes.c_int
+    pd, pb = ctypes.POINTER(PagedDesc), ctypes.POINTER(_PagedBatch)
+    L.kvc_validate_paged_desc.argtypes = [pd]
+    L.kvc_validate_paged_desc.restype = ctypes.c_int
+    L.kvc_attend_ws_bytes.argtypes = [pd, pb]
+    L.kvc_attend_ws_bytes.restype = u64
+    L.kvc_append.argtypes = [pd, pb, u32, vp, vp, u64, vp, u64, vp, u64, vp, u64,
+                             ctypes.POINTER(_RopeArgs), vp, vp]
+    L.kvc_append.restype = ctypes.c_int
+    for name in ("kvc_attend", "kvc_attend_prompt"):
+        getattr(L, name).argtypes = [pd, pb, u32, vp, vp, u64, ctypes.c_float, u32, vp, u64, vp,
+                                     vp, u64, vp, vp]
+        getattr(L, name).restype = ctypes.c_int
+    L.kvc_page_out.argtypes = [pd, vp, vp, u32, u32, u32, vp, u32, u32, vp, vp]
+    L.kvc_page_out.restype = ctypes.c_int
+    L.kvc_page_in.argtypes = [pd, vp, u32, u32, vp, vp, u32, u32, u32, vp, vp]
+    L.kvc_page_in.restype = ctypes.c_int
     _lib = L
     return L
 
@@ -739,3 +801,222 @@ def decode_refined(desc: CodecDesc, tables: torch.Tensor, rtables: torch.Tensor,
     decode_refined_async(desc, tables, rtables, refine_bits, refs, out, wsp, stream)
     read_status(wsp.status, "kvc_decode_refined", stream)
     return out
+
+
+# -------------------------------------------------------------- paged KV cache
+_KVC_DTYPE = {torch.float16: 0, torch.bfloat16: 1}
+_DTYPES = (torch.float16, torch.bfloat16)
+
+
+def make_paged_desc(n_layers: int, n_heads: int, n_kv_heads: int, head_dim: int, page_tokens: int,
+                    n_pages: int, cache_dtype: torch.dtype = torch.float16,
+                    io_dtype: Optional[torch.dtype] = None) -> PagedDesc:
+    """A pool [n_layers][2][n_pages * page_tokens][n_kv_heads * head_dim] of
+    cache_dtype, read by n_heads query heads; io_dtype (default: the cache's)
+    is the type of q, k, v and the attention's output."""
+    io_dtype = cache_dtype if io_dtype is None else io_dtype
+    if cache_dtype not in _KVC_DTYPE or io_dtype not in _KVC_DTYPE:
+        raise KvcError(ERR_INVALID_ARG, "make_paged_desc")
+    p = PagedDesc(n_layers, n_heads, n_kv_heads, head_dim, page_tokens, n_pages,
+                  _KVC_DTYPE[cache_dtype], _KVC_DTYPE[io_dtype])
+    _check(lib().kvc_validate_paged_desc(ctypes.byref(p)), "make_paged_desc")
+    return p
+
+
+def _int32_tensor(t: torch.Tensor, dims: int, what: str) -> torch.Tensor:
+    if not t.is_cuda or t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dims}-dimensional int32 CUDA tensor")
+    return t
+
+
+class PagedBatch:
+    """kvc_paged_batch: page table [n_seqs][entries], cache lengths [n_seqs]
+    (the new tokens included) and, for several new tokens a sequence, q_start
+    [n_seqs + 1].  Kept across layers and steps: the tensors' contents may
+    change between calls (lengths grow, pages are handed out), the tensors
+    themselves stay.  max_len bounds every length for the batch's whole life
+    (default: what the table can hold)."""
+
+    def __init__(self, table: torch.Tensor, lens: torch.Tensor,
+                 q_start: Optional[torch.Tensor] = None, max_len: Optional[int] = None):
+        self.table = _int32_tensor(table, 2, "table")
+        self.lens = _int32_tensor(lens, 1, "lens")
+        self.q_start = None if q_start is None else _int32_tensor(q_start, 1, "q_start")
+        self.n_seqs = lens.shape[0]
+        if table.shape[0] != self.n_seqs:
+            raise ValueError("table must have a row for each sequence")
+        if q_start is not None and q_start.shape[0] != self.n_seqs + 1:
+            raise ValueError("q_start must have n_seqs + 1 entries")
+        if any(t is not None and t.device != table.device for t in (lens, q_start)):
+            raise ValueError("the batch's tensors must be on one device")
+        self.device = table.device
+        self.max_len = max_len
+
+    def _args(self, desc: PagedDesc, n_tokens: int) -> _PagedBatch:
+        most = self.table.shape[1] * desc.page_tokens
+        q = self.q_start
+        return _PagedBatch(self.table.data_ptr(), self.lens.data_ptr(),
+                           None if q is None else q.data_ptr(), self.n_seqs, self.table.shape[1],
+                           n_tokens, min(most, 2**31 - 1) if self.max_len is None
+                           else self.max_len)
+
+
+class PagedWorkspace:
+    """Scratch memory and status word of the paged calls for batches of these
+    sizes: n_tokens rows of new tokens (default: one for each sequence)."""
+
+    def __init__(self, desc: PagedDesc, batch: PagedBatch, n_tokens: Optional[int] = None):
+        b = batch._args(desc, batch.n_seqs if n_tokens is None else n_tokens)
+        self.ws_bytes = int(lib().kvc_attend_ws_bytes(ctypes.byref(desc), ctypes.byref(b)))
+        self.ws = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=batch.device)
+        self.status = _dev_status(batch.device)
+
+
+def rope_table(n_positions: int, rotary_dim: int, base: float = 10000.0,
+               device="cuda") -> torch.Tensor:
+    """cos_sin [n_positions][rotary_dim] of angles position * base^(-2i /
+    rotary_dim), taken in binary64 and rounded once."""
+    i = torch.arange(0, rotary_dim, 2, dtype=torch.float64)
+    ang = torch.arange(n_positions, dtype=torch.float64)[:, None] * base ** (-i / rotary_dim)
+    return torch.cat([ang.cos(), ang.sin()], 1).float().contiguous().to(device)
+
+
+class Rope:
+    """kvc_rope: cos_sin [n_positions][rotary_dim] binary32 (cosines, then
+    sines); pairs (j, j + rotary_dim / 2), or (2j, 2j + 1) if interleaved."""
+
+    def __init__(self, cos_sin: torch.Tensor, interleaved: bool = False):
+        if (not cos_sin.is_cuda or cos_sin.dtype != torch.float32 or cos_sin.dim() != 2
+                or not cos_sin.is_contiguous()):
+            raise ValueError("cos_sin must be a contiguous [n_positions][rotary_dim] float32 "
+                             "CUDA tensor")
+        self.cos_sin = cos_sin
+        self.interleaved = bool(interleaved)
+
+    def _args(self) -> _RopeArgs:
+        t = self.cos_sin
+        return _RopeArgs(t.data_ptr(), t.shape[0], t.shape[1], int(self.interleaved), 0)
+
+
+def _pool_ptr(desc: PagedDesc, pool: torch.Tensor, device) -> int:
+    if tuple(pool.shape) != desc.pool_shape or pool.device != device:
+        raise ValueError(f"the pool must have shape {desc.pool_shape} and the batch's device")
+    if pool.dtype != torch.int16 and pool.dtype != _DTYPES[desc.cache_dtype]:
+        raise ValueError("the pool's type differs from the descriptor's")
+    return _kv_ptr(pool)
+
+
+def _token_rows(t: torch.Tensor, n: int, heads: int, desc: PagedDesc, device, what: str) -> int:
+    """Checks [n][heads][head_dim] rows and returns their token stride."""
+    s = t.stride()
+    if (tuple(t.shape) != (n, heads, desc.head_dim) or t.dtype != _DTYPES[desc.io_dtype]
+            or t.device != device or s[2] != 1 or (heads > 1 and s[1] != desc.head_dim)):
+        raise ValueError(f"{what} must be [{n}][{heads}][{desc.head_dim}] rows of the "
+                         "descriptor's io type on the batch's device, each row contiguous")
+    return s[0] if n > 1 else heads * desc.head_dim
+
+
+def _paged_stream(stream: Optional[torch.cuda.Stream], device) -> ctypes.c_void_p:
+    if device.index != torch.cuda.current_device():
+        raise ValueError("the tensors' device must be the current one")
+    return _stream(stream)
+
+
+def append_async(desc: PagedDesc, batch: PagedBatch, layer: int, pool: torch.Tensor,
+                 k: torch.Tensor, v: torch.Tensor, wsp: PagedWorkspace,
+                 rope: Optional[Rope] = None, q: Optional[torch.Tensor] = None,
+                 q_out: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Launch kvc_append: the batch's new tokens k, v [n_tokens][n_kv_heads]
+    [head_dim] into their slots of `layer`, keys (and queries q into q_out)
+    turned by rope (no sync; device errors stay in wsp.status)."""
+    dev = batch.device
+    n = k.shape[0]
+    b = batch._args(desc, n)
+    ks = _token_rows(k, n, desc.n_kv_heads, desc, dev, "k")
+    vs = _token_rows(v, n, desc.n_kv_heads, desc, dev, "v")
+    qs = os_ = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        qs = _token_rows(q, n, desc.n_heads, desc, dev, "q")
+        os_ = _token_rows(q_out, n, desc.n_heads, desc, dev, "q_out")
+    if rope is not None and rope.cos_sin.device != dev:
+        raise ValueError("the rotation table must be on the batch's device")
+    _check(lib().kvc_append(desc, b, layer, _pool_ptr(desc, pool, dev), k.data_ptr(), ks,
+                            v.data_ptr(), vs, None if q is None else q.data_ptr(), qs,
+                            None if q is None else q_out.data_ptr(), os_,
+                            None if rope is None else rope._args(), wsp.status.data_ptr(),
+                            _paged_stream(stream, dev)), "kvc_append")
+
+
+def _attend(name: str, desc: PagedDesc, batch: PagedBatch, layer: int, pool, q, out, wsp, scale,
+            window, lse, stream) -> None:
+    dev = batch.device
+    n = q.shape[0]
+    b = batch._args(desc, n)
+    qs = _token_rows(q, n, desc.n_heads, desc, dev, "q")
+    os_ = _token_rows(out, n, desc.n_heads, desc, dev, "out")
+    if lse is not None and (tuple(lse.shape) != (n, desc.n_heads) or lse.device != dev
+                            or lse.dtype != torch.float32 or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous [n_tokens][n_heads] float32 tensor")
+    if window < 0:
+        raise ValueError("window must not be negative")
+    if wsp.ws.device != dev:
+        raise ValueError("the workspace must be on the batch's device")
+    _check(getattr(lib(), name)(desc, b, layer, _pool_ptr(desc, pool, dev), q.data_ptr(), qs,
+                                desc.head_dim ** -0.5 if scale is None else scale, window,
+                                out.data_ptr(), os_, None if lse is None else lse.data_ptr(),
+                                wsp.ws.data_ptr(), wsp.ws_bytes, wsp.status.data_ptr(),
+                                _paged_stream(stream, dev)), name)
+
+
+def attend_async(desc: PagedDesc, batch: PagedBatch, layer: int, pool: torch.Tensor,
+                 q: torch.Tensor, out: torch.Tensor, wsp: PagedWorkspace,
+                 scale: Optional[float] = None, window: int = 0,
+                 lse: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Launch kvc_attend: each sequence's one new token q [n_seqs][n_heads]
+    [head_dim] over its cache, into out (and the log-sum-exp into lse
+    [n_seqs][n_heads]).  scale defaults to head_dim^-1/2 (no sync)."""
+    _attend("kvc_attend", desc, batch, layer, pool, q, out, wsp, scale, window, lse, stream)
+
+
+def attend_prompt_async(desc: PagedDesc, batch: PagedBatch, layer: int, pool: torch.Tensor,
+                        q: torch.Tensor, out: torch.Tensor, wsp: PagedWorkspace,
+                        scale: Optional[float] = None, window: int = 0,
+                        lse: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Launch kvc_attend_prompt: several new tokens a sequence (batch.q_start),
+    each over the tokens up to its own position (no sync)."""
+    _attend("kvc_attend_prompt", desc, batch, layer, pool, q, out, wsp, scale, window, lse, stream)
+
+
+def _page_args(desc: PagedDesc, pool, table, flat, status):
+    dev = pool.device
+    _int32_tensor(table, 1, "table")
+    _int32_tensor(status, 1, "status")
+    shape = (desc.n_layers, 2, flat.shape[2], desc.n_kv_heads * desc.head_dim)
+    if tuple(flat.shape) != shape or any(t.device != dev for t in (table, flat, status)):
+        raise ValueError(f"the tensor must have shape {shape} and the pool's device")
+    return dev, _pool_ptr(desc, pool, dev), _kv_ptr(flat)
+
+
+def page_out_async(desc: PagedDesc, pool: torch.Tensor, table: torch.Tensor, first_token: int,
+                   n_tokens: int, out: torch.Tensor, out_first: int, status: torch.Tensor,
+                   stream=None) -> None:
+    """Launch kvc_page_out: tokens [first_token, first_token + n_tokens) of the
+    sequence with page ids `table`, every layer, into out [L][2][T][C] from
+    token out_first on (no sync; device errors stay in status)."""
+    dev, pp, fp = _page_args(desc, pool, table, out, status)
+    _check(lib().kvc_page_out(desc, pp, table.data_ptr(), table.shape[0], first_token, n_tokens,
+                              fp, out.shape[2], out_first, status.data_ptr(),
+                              _paged_stream(stream, dev)), "kvc_page_out")
+
+
+def page_in_async(desc: PagedDesc, kv: torch.Tensor, in_first: int, pool: torch.Tensor,
+                  table: torch.Tensor, first_token: int, n_tokens: int, status: torch.Tensor,
+                  stream=None) -> None:
+    """Launch kvc_page_in: kv [L][2][T][C], tokens from in_first on, into the
+    sequence's tokens [first_token, first_token + n_tokens) (no sync)."""
+    dev, pp, fp = _page_args(desc, pool, table, kv, status)
+    _check(lib().kvc_page_in(desc, fp, kv.shape[2], in_first, pp, table.data_ptr(),
+                             table.shape[0], first_token, n_tokens, status.data_ptr(),
+                             _paged_stream(stream, dev)), "kvc_page_in")

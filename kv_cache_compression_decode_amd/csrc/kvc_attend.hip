@@ -1,0 +1,539 @@
+// Attention of new tokens over the paged KV cache.
+//
+// A row is one (new token, query head); the rows of one sequence that share a
+// KV head are (token, head in group) pairs r = i * group + g.  For a row at
+// position p, with s_j = scale q.k_j over its visible tokens j,
+//   m = max s_j,  l = sum exp(s_j - m),  out = sum exp(s_j - m) v_j / l,
+// computed in one pass over the keys and values with a running m: the sums so
+// far are multiplied by exp(m_old - m_new) when the maximum grows.
+#include <algorithm>
+
+#include "kvc_paged.h"
+
+namespace kvc {
+namespace {
+
+typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// D = A B + C on 16 x 16 tiles over 32 products.  Lane l holds of A row l%16
+// and of B column l%16, products (l/16)*8 .. +7 of both; of C and D column
+// l%16, rows (l/16)*4 .. +3.
+template <class T>
+__device__ inline f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (std::is_same<T, f16>::value)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+constexpr float kLn2 = 0.69314718055994530942f;
+__device__ inline float ninf() { return -__builtin_inff(); }
+
+// The probabilities are rounded to the cache's type for the second product,
+// half a step of that type each (2^-11 or 2^-8 relative), while their sum l
+// is taken in binary32 before the rounding.  A binary16 probability is
+// scaled by 2^14 (added to the exponent, so l carries it too and it cancels
+// in the quotient): its smallest step becomes 2^-38 of the largest
+// probability instead of 2^-24, so a long tail of small ones is not lost.
+template <class T>
+constexpr float kShift = std::is_same<T, f16>::value ? 14.0f : 0.0f;
+
+// 8 consecutive elements of a query row in the cache's type.
+template <class TI, class TC>
+__device__ inline u32x4 load_q8(const TI *p) {
+  u32x4 w = load16(p);
+  if constexpr (!std::is_same<TI, TC>::value) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = pack2<TC>(elem_lo<TI>(w[i]), elem_hi<TI>(w[i]));
+  }
+  return w;
+}
+
+// N dwords from a 4-byte aligned address (more where N allows it).
+template <int N>
+struct Words {
+  uint32_t w[N];
+};
+template <int N>
+__device__ inline Words<N> load_words(const void *p) {
+  Words<N> r;
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const u32x4 v = load16(static_cast<const uint32_t *>(p) + 4 * i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r.w[4 * i + e] = v[e];
+    }
+  } else if constexpr (N == 3) {
+    typedef uint32_t u32x3 __attribute__((ext_vector_type(3), aligned(4)));
+    const u32x3 v = *static_cast<const u32x3 *>(p);
+    r.w[0] = v[0];
+    r.w[1] = v[1];
+    r.w[2] = v[2];
+  } else {
+    static_assert(N == 2, "head dimension");
+    const u32x2 v = *static_cast<const u32x2 *>(p);
+    r.w[0] = v[0];
+    r.w[1] = v[1];
+  }
+  return r;
+}
+
+// A dword holds two elements: is either an infinity or NaN?
+template <class T>
+__device__ inline bool nonfinite2(uint32_t w) {
+  constexpr uint32_t e = std::is_same<T, f16>::value ? 0x7C00u : 0x7F80u;
+  return (w & e) == e || (w & (e << 16)) == (e << 16);
+}
+
+// ------------------------------------------------------------ row tiles
+// Row tile `t` of the launch: rows [first, first + rows) of sequence b, in
+// sequence order, every sequence's rows cut into tiles of kRows.
+struct Tile {
+  uint32_t b, row0, n;  // the sequence, its first token row and token count
+  uint32_t first, rows;
+};
+
+// Each wave finds the tile by itself: 64 sequences at a time, a scan of
+// their tile counts.  False if the batch has fewer tiles.
+template <uint32_t kRows>
+__device__ inline bool find_tile(const AttendArgs &a, uint32_t t, Tile &out) {
+  const uint32_t lane = threadIdx.x & 63;
+  if (a.s.q_start == nullptr) {  // one token each: the same number of tiles for all
+    const uint32_t per = (a.group + kRows - 1) / kRows;
+    out.b = t / per;
+    if (out.b >= a.s.n_seqs) return false;
+    out.row0 = out.b;
+    out.n = 1;
+    out.first = (t - out.b * per) * kRows;
+    out.rows = min(kRows, a.group - out.first);
+    return true;
+  }
+  uint32_t base = 0;
+  for (uint32_t b0 = 0; b0 < a.s.n_seqs; b0 += 64) {
+    uint32_t row0 = 0, n = 0;
+    const uint32_t b = b0 + lane;
+    if (b < a.s.n_seqs) {
+      a.s.rows(b, row0, n);
+      if (t == 0 && a.s.rows_bad(b)) set_status(a.status, KVC_ERR_SHAPE);
+    }
+    const uint32_t mine = (n * a.group + kRows - 1) / kRows;
+    uint32_t sum = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t o = __shfl_up(sum, d);
+      if (lane >= (uint32_t)d) sum += o;
+    }
+    const uint64_t above = __ballot(base + sum > t);
+    if (above) {
+      const int src = __builtin_ctzll(above);
+      out.b = b0 + (uint32_t)src;
+      out.row0 = __shfl(row0, src);
+      out.n = __shfl(n, src);
+      const uint32_t k = t - base - __shfl(sum - mine, src);
+      out.first = k * kRows;
+      if (out.first >= out.n * a.group) return false;  // only if q_start overlaps itself
+      out.rows = min(kRows, out.n * a.group - out.first);
+      return true;
+    }
+    base += __shfl(sum, 63);
+  }
+  return false;
+}
+
+// Where a row writes, and its visible tokens [lo, hi).
+struct Row {
+  uint32_t token, head;  // row of q and out; head within the group
+  int32_t lo, hi;
+};
+__device__ inline Row row_of(const AttendArgs &a, const Tile &t, int32_t len, uint32_t r) {
+  Row w;
+  const uint32_t i = r / a.group;
+  w.head = r - i * a.group;
+  w.token = t.row0 + i;
+  const int32_t pos = len - (int32_t)t.n + (int32_t)i;
+  w.hi = pos < 0 ? 0 : pos + 1;
+  w.lo = a.window != 0 && (uint32_t)w.hi > a.window ? w.hi - (int32_t)a.window : 0;
+  return w;
+}
+
+// ------------------------------------------------------- 16 rows a workgroup
+// The four waves of a workgroup share 16 rows and take tiles of 32 tokens in
+// turn; they are joined through LDS at the end.  With `splits` workgroups to
+// a row tile, each takes an equal share of the tokens and writes its sums,
+// maximum and unnormalised output to the workspace for k_attend_join.
+//
+// Scores are computed transposed, S^T = K Q^T: lane l holds row l%16's scores
+// of tokens (l/16)*4 .. +3 of both halves of the tile.  That is the layout in
+// which the second product O^T = V^T P^T wants P^T, if product k = (l/16)*8+j
+// stands for token (l/16)*4 + j of the first half (j < 4) or (l/16)*4 + j - 4
+// of the second: P never leaves its lane.  V^T wants, for the same eight
+// tokens, one dimension a lane: a lane loads E = head_dim/16 consecutive
+// dimensions of its eight tokens (16 lanes cover whole rows, so the loads are
+// contiguous) and the i-th product takes dimension l%16 * E + i, a byte
+// permutation in registers.  Neither K nor V passes through LDS.
+constexpr uint32_t kTok = 32;
+
+template <class TI, class TC, int D>
+__global__ __launch_bounds__(256) void k_attend_rows(AttendArgs a) {
+  constexpr int E = D / 16;
+  constexpr int KK = D / 32;
+  constexpr int EC = E < 8 ? E : 8;  // dimensions a lane joins at a time
+  __shared__ float s_o[4][16][16 * EC + 4];
+  __shared__ float s_m[4][16], s_l[4][16];
+  const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const uint32_t n16 = lane & 15, g4 = lane >> 4;
+  const uint32_t hk = blockIdx.x % a.n_kv_heads;
+  const uint32_t rest = blockIdx.x / a.n_kv_heads;
+  const uint32_t split = rest % a.splits, tile = rest / a.splits;
+  Tile t;
+  if (!find_tile<16>(a, tile, t)) return;
+  const int32_t len = a.s.len(t.b);
+  if (wave == 0 && lane == 0 && a.s.len_bad(t.b)) set_status(a.status, KVC_ERR_SHAPE);
+  // this lane's row, and the tile's token range
+  const bool live = n16 < t.rows;
+  const Row row = row_of(a, t, len, t.first + (live ? n16 : 0));
+  const Row r_first = row_of(a, t, len, t.first), r_last = row_of(a, t, len, t.first + t.rows - 1);
+  const int32_t begin = r_first.lo, end = r_last.hi;  // lo and hi grow with the row
+  const int32_t n_tiles = end > begin ? (end - begin + (int32_t)kTok - 1) / (int32_t)kTok : 0;
+  const int32_t t_lo = (int32_t)((int64_t)n_tiles * split / a.splits);
+  const int32_t t_hi = (int32_t)((int64_t)n_tiles * (split + 1) / a.splits);
+  const uint32_t qh = hk * a.group + row.head;
+
+  u32x4 qf[KK];
+#pragma unroll
+  for (int kk = 0; kk < KK; ++kk) qf[kk] = u32x4{0, 0, 0, 0};
+  if (live) {
+    const TI *q = static_cast<const TI *>(a.q) + (uint64_t)row.token * a.q_stride +
+                  (uint64_t)qh * D + g4 * 8;
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) qf[kk] = load_q8<TI, TC>(q + kk * 32);
+  }
+
+  float m = ninf(), l = 0.0f;
+  f32x4 o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = f32x4{0, 0, 0, 0};
+  const int32_t *table = a.s.table + (uint64_t)t.b * a.s.table_stride;
+  const TC *kbase = static_cast<const TC *>(a.k) + (uint64_t)hk * D;
+  const TC *vbase = static_cast<const TC *>(a.v) + (uint64_t)hk * D;
+  const int32_t last = end - 1;
+  bool bad = false;
+
+  for (int32_t ti = t_lo + (int32_t)wave; ti < t_hi; ti += 4) {
+    const int32_t j0 = begin + ti * (int32_t)kTok;
+    // slots of this lane's two key rows and eight value rows
+    uint32_t kslot[2], vslot[8];
+    {
+      // each lane looks up one token of the tile; the others' come by shuffle
+      int32_t j = j0 + (int32_t)(lane & 31);
+      j = j < last ? j : last;
+      uint32_t slot;
+      bad = !slot_of(table, a.s.page, a.s.n_pages, (uint32_t)j, slot) || bad;
+      kslot[0] = __shfl(slot, n16);
+      kslot[1] = __shfl(slot, 16 + n16);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) vslot[i] = __shfl(slot, (i >> 2) * 16 + g4 * 4 + (i & 3));
+    }
+    u32x4 kf[2][KK];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const TC *kp = kbase + (uint64_t)kslot[h] * a.row + g4 * 8;
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) kf[h][kk] = load16(kp + kk * 32);
+    }
+    Words<E / 2> vf[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      vf[i] = load_words<E / 2>(vbase + (uint64_t)vslot[i] * a.row + n16 * E);
+
+    f32x4 sc[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      sc[h] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) sc[h] = mfma16<TC>(kf[h][kk], qf[kk], sc[h]);
+    }
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = sc[i >> 2][i & 3] * a.scale;
+    // some token of the tile is hidden from some row
+    const bool edge = j0 < r_last.lo || j0 + (int32_t)kTok > r_first.hi;
+    if (edge) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int32_t j = j0 + (i >> 2) * 16 + (int32_t)g4 * 4 + (i & 3);
+        x[i] = j >= row.lo && j < row.hi ? x[i] : ninf();
+      }
+    }
+    float mt = x[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) mt = __builtin_fmaxf(mt, x[i]);
+    mt = __builtin_fmaxf(mt, __shfl_xor(mt, 16));
+    mt = __builtin_fmaxf(mt, __shfl_xor(mt, 32));
+    const float mn = __builtin_fmaxf(m, mt);
+    const float ref = mn == ninf() ? 0.0f : mn;  // nothing visible yet: exp2(-inf - 0) = 0
+    const float alpha = __builtin_amdgcn_exp2f(m - ref);
+    m = mn;
+    float p[8];
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      p[i] = __builtin_amdgcn_exp2f(x[i] - ref + kShift<TC>);
+      sum += p[i];
+    }
+    l = __builtin_fmaf(l, alpha, sum);
+    u32x4 pf;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pf[i] = pack2<TC>(p[2 * i], p[2 * i + 1]);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= alpha;
+
+    if (edge) {
+      // A hidden token's probability is 0, but 0 times an infinity or NaN of
+      // its value row is not: tokens hidden from every row are zeroed here,
+      // and a token that some rows see and others do not (its row of V not
+      // finite) is taken out of the product and added lane by lane, where
+      // the row's own visibility decides.
+      bool odd = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int32_t j = j0 + (i >> 2) * 16 + (int32_t)g4 * 4 + (i & 3);
+        bool nf = false;
+#pragma unroll
+        for (int w = 0; w < E / 2; ++w) {
+          if (j >= end || j < begin) vf[i].w[w] = 0;
+          nf = nf || nonfinite2<TC>(vf[i].w[w]);
+        }
+        odd = odd || nf;
+      }
+      if (__ballot(odd)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          bool nf = false;
+#pragma unroll
+          for (int w = 0; w < E / 2; ++w) nf = nf || nonfinite2<TC>(vf[i].w[w]);
+          const uint64_t who = __ballot(nf);
+          for (uint32_t g = 0; g < 4; ++g) {
+            if (((who >> (16 * g)) & 0xFFFFu) == 0) continue;
+            // token (half, g, i): its probability for this lane's row is in
+            // lane g*16 + n16; its values at this lane's output dimensions
+            const int32_t j = j0 + (i >> 2) * 16 + (int32_t)g * 4 + (i & 3);
+            const float pj = __shfl(p[i], (int)(g * 16 + n16));
+            const uint32_t sj = __shfl(vslot[i], (int)(g * 16));
+            if (g4 == g) {
+#pragma unroll
+              for (int w = 0; w < E / 2; ++w) vf[i].w[w] = 0;
+            }
+            if (j >= row.lo && j < row.hi) {
+              const TC *vp = vbase + (uint64_t)sj * a.row;
+#pragma unroll
+              for (int e = 0; e < E; ++e)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                  o[e][c] = __builtin_fmaf(pj, (float)vp[(g4 * 4 + c) * E + e], o[e][c]);
+            }
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      u32x4 vt;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        vt[i] = __builtin_amdgcn_perm(vf[2 * i + 1].w[e / 2], vf[2 * i].w[e / 2],
+                                      (e & 1) ? 0x07060302u : 0x05040100u);
+      o[e] = mfma16<TC>(vt, pf, o[e]);
+    }
+  }
+  if (__ballot(bad) && lane == 0) set_status(a.status, KVC_ERR_SHAPE);
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+
+  // join the waves: each one's sums times exp2(its maximum - the common one)
+  if (lane < 16) {
+    s_m[wave][lane] = m;
+    s_l[wave][lane] = l;
+  }
+  __syncthreads();
+  float mm = ninf();
+#pragma unroll
+  for (int w = 0; w < 4; ++w) mm = __builtin_fmaxf(mm, s_m[w][n16]);
+  const float mref = mm == ninf() ? 0.0f : mm;
+  const float f = __builtin_amdgcn_exp2f(m - mref);
+  const bool single = a.splits == 1;
+  const uint64_t part = ((uint64_t)tile * a.n_kv_heads + hk) * a.splits + split;
+#pragma unroll
+  for (int e0 = 0; e0 < E; e0 += EC) {
+    if (e0) __syncthreads();
+#pragma unroll
+    for (int e = 0; e < EC; ++e)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        s_o[wave][n16][(g4 * 4 + c) * EC + e] = o[e0 + e][c] * f;
+    __syncthreads();
+    // 16 rows of 16 * EC dimensions, two at a time; dimension k * E + e0 + e
+    for (uint32_t i = threadIdx.x; i < 16u * 8u * EC; i += 256) {
+      const uint32_t r = i / (8u * EC), x = (i - r * (8u * EC)) * 2;
+      if (r >= t.rows) continue;
+      float v0 = 0.0f, v1 = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        v0 += s_o[w][r][x];
+        v1 += s_o[w][r][x + 1];
+      }
+      const uint32_t dim = E == EC ? x : (x / EC) * E + e0 + x % EC;
+      if (single) {
+        float mr = ninf(), lr = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) mr = __builtin_fmaxf(mr, s_m[w][r]);
+        const float rr = mr == ninf() ? 0.0f : mr;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) lr += s_l[w][r] * __builtin_amdgcn_exp2f(s_m[w][r] - rr);
+        const Row w = row_of(a, t, len, t.first + r);
+        const bool some = w.hi > w.lo;
+        const float inv = some ? 1.0f / lr : 0.0f;
+        const uint32_t h = hk * a.group + w.head;
+        uint32_t *op = reinterpret_cast<uint32_t *>(static_cast<TI *>(a.out) +
+                                                    (uint64_t)w.token * a.out_stride +
+                                                    (uint64_t)h * D + dim);
+        *op = some ? pack2<TI>(v0 * inv, v1 * inv) : 0u;
+        if (x == 0 && e0 == 0 && a.lse)
+          a.lse[(uint64_t)w.token * a.n_heads + h] =
+              some ? (mr - kShift<TC> + __builtin_amdgcn_logf(lr)) * kLn2 : ninf();
+      } else {
+        float *op = a.part + (part * 16 + r) * D + dim;
+        op[0] = v0;
+        op[1] = v1;
+      }
+    }
+  }
+  if (!single && threadIdx.x < 16) {
+    float lr = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) lr += s_l[w][n16] * __builtin_amdgcn_exp2f(s_m[w][n16] - mref);
+    a.part_ml[part * 32 + n16] = mm;
+    a.part_ml[part * 32 + 16 + n16] = lr;
+  }
+}
+
+// Joins the splits of a row: a wave per (row tile, KV head, row).
+template <class TI, class TC, int D>
+__global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
+  const uint32_t lane = threadIdx.x & 63;
+  const uint32_t unit = blockIdx.x / 4, r = (blockIdx.x % 4) * 4 + (threadIdx.x >> 6);
+  const uint32_t hk = unit % a.n_kv_heads, tile = unit / a.n_kv_heads;
+  Tile t;
+  if (!find_tile<16>(a, tile, t)) return;
+  if (r >= t.rows) return;
+  const Row row = row_of(a, t, a.s.len(t.b), t.first + r);
+  const uint64_t part = ((uint64_t)tile * a.n_kv_heads + hk) * a.splits;
+  float mm = ninf();
+  for (uint32_t s = lane; s < a.splits; s += 64)
+    mm = __builtin_fmaxf(mm, a.part_ml[(part + s) * 32 + r]);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) mm = __builtin_fmaxf(mm, __shfl_xor(mm, d));
+  const float ref = mm == ninf() ? 0.0f : mm;
+  float acc[(D + 127) / 128 * 2] = {};
+  float l = 0.0f;
+  for (uint32_t s = 0; s < a.splits; ++s) {
+    const float f = __builtin_amdgcn_exp2f(a.part_ml[(part + s) * 32 + r] - ref);
+    l = __builtin_fmaf(a.part_ml[(part + s) * 32 + 16 + r], f, l);
+    const float *op = a.part + ((part + s) * 16 + r) * D;
+#pragma unroll
+    for (int k = 0; k < (D + 127) / 128; ++k) {
+      const uint32_t dim = (lane + 64 * k) * 2;
+      if (dim < D) {
+        acc[2 * k] = __builtin_fmaf(op[dim], f, acc[2 * k]);
+        acc[2 * k + 1] = __builtin_fmaf(op[dim + 1], f, acc[2 * k + 1]);
+      }
+    }
+  }
+  const bool some = row.hi > row.lo;
+  const float inv = some ? 1.0f / l : 0.0f;
+  const uint32_t h = hk * a.group + row.head;
+  uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<TI *>(a.out) +
+                                               (uint64_t)row.token * a.out_stride +
+                                               (uint64_t)h * D);
+#pragma unroll
+  for (int k = 0; k < (D + 127) / 128; ++k) {
+    const uint32_t dim = (lane + 64 * k) * 2;
+    if (dim < D) out[dim / 2] = some ? pack2<TI>(acc[2 * k] * inv, acc[2 * k + 1] * inv) : 0u;
+  }
+  if (lane == 0 && a.lse)
+    a.lse[(uint64_t)row.token * a.n_heads + h] =
+        some ? (mm - kShift<TC> + __builtin_amdgcn_logf(l)) * kLn2 : ninf();
+}
+
+// ------------------------------------------------------------------- host
+struct Plan {
+  uint32_t tiles, splits;
+  uint64_t part, part_ml, total;  // workspace offsets
+};
+
+Plan make_plan(const kvc_paged_desc &p, const kvc_paged_batch &b) {
+  Plan w{};
+  const uint32_t group = p.n_heads / p.n_kv_heads;
+  // every sequence's last tile may be partly filled
+  w.tiles = b.q_start ? (uint32_t)((uint64_t)b.n_tokens * group / 16) +
+                            std::min(b.n_seqs, b.n_tokens)
+                      : b.n_seqs * ((group + 15) / 16);
+  const uint64_t units = (uint64_t)w.tiles * p.n_kv_heads;
+  // enough workgroups for the 256 CUs, three to each, but at least 256
+  // tokens to a split
+  const uint64_t want = (3 * 256 + units - 1) / std::max<uint64_t>(units, 1);
+  w.splits = (uint32_t)std::max<uint64_t>(
+      1, std::min<uint64_t>(want, ((uint64_t)b.max_len + 255) / 256));
+  if (w.splits > 1) {
+    const uint64_t n = units * w.splits;
+    w.part_ml = n * 16 * p.head_dim * 4;
+    w.total = w.part_ml + n * 32 * 4;
+    w.total = (w.total + 255) & ~uint64_t(255);
+  }
+  return w;
+}
+
+template <class TI, class TC, int D>
+hipError_t launch_d(const kvc_paged_desc &p, const AttendArgs &a, hipStream_t stream) {
+  const uint32_t units = a.tiles * a.n_kv_heads;
+  hipLaunchKernelGGL((k_attend_rows<TI, TC, D>), dim3(units * a.splits), dim3(256), 0,
+                     stream, a);
+  if (a.splits > 1)
+    hipLaunchKernelGGL((k_attend_join<TI, TC, D>), dim3(units * 4), dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
+template <class TI, class TC>
+hipError_t launch_t(const kvc_paged_desc &p, const AttendArgs &a, hipStream_t stream) {
+  switch (p.head_dim) {
+    case 64: return launch_d<TI, TC, 64>(p, a, stream);
+    case 96: return launch_d<TI, TC, 96>(p, a, stream);
+    case 128: return launch_d<TI, TC, 128>(p, a, stream);
+    default: return launch_d<TI, TC, 256>(p, a, stream);
+  }
+}
+
+}  // namespace
+
+uint64_t attend_ws_bytes(const kvc_paged_desc &p, const kvc_paged_batch &b) {
+  return make_plan(p, b).total;
+}
+
+hipError_t launch_attend(const kvc_paged_desc &p, const kvc_paged_batch &b, AttendArgs a, void *ws,
+                         hipStream_t stream) {
+  const Plan w = make_plan(p, b);
+  a.tiles = w.tiles;
+  a.splits = w.splits;
+  uint8_t *base = static_cast<uint8_t *>(ws);
+  a.part = reinterpret_cast<float *>(base + w.part);
+  a.part_ml = reinterpret_cast<float *>(base + w.part_ml);
+  if (p.io_dtype == KVC_F16) return launch_t<f16, f16>(p, a, stream);
+  if (p.cache_dtype == KVC_BF16) return launch_t<bf16, bf16>(p, a, stream);
+  return launch_t<bf16, f16>(p, a, stream);
+}
+
+}  // namespace kvc

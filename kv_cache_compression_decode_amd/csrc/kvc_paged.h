@@ -1,0 +1,141 @@
+// Definitions shared by the paged-cache kernels and their host code.
+#pragma once
+
+#include "kvc_internal.h"
+
+namespace kvc {
+
+// Element types inside the kernels.
+typedef _Float16 f16;
+typedef __bf16 bf16;
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// 16 bytes of a 16-byte aligned address.
+__device__ inline u32x4 load16(const void *p) { return *reinterpret_cast<const u32x4 *>(p); }
+__device__ inline void store16(void *p, u32x4 v) { *reinterpret_cast<u32x4 *>(p) = v; }
+
+// The two elements of a dword, widened (both types widen exactly).
+template <class T>
+__device__ inline float elem_lo(uint32_t w);
+template <class T>
+__device__ inline float elem_hi(uint32_t w);
+template <>
+__device__ inline float elem_lo<f16>(uint32_t w) { return h2f((uint16_t)w); }
+template <>
+__device__ inline float elem_hi<f16>(uint32_t w) { return h2f((uint16_t)(w >> 16)); }
+template <>
+__device__ inline float elem_lo<bf16>(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
+template <>
+__device__ inline float elem_hi<bf16>(uint32_t w) {
+  return __builtin_bit_cast(float, w & 0xFFFF0000u);
+}
+
+// Two binary32 values rounded to nearest even in a dword of T.  (The hardware
+// conversion to bfloat16 takes two values; NaN stays NaN.)
+template <class T>
+__device__ inline uint32_t pack2(float a, float b) {
+  typedef T pair __attribute__((ext_vector_type(2)));
+  pair r;
+  r[0] = (T)a;
+  r[1] = (T)b;
+  return __builtin_bit_cast(uint32_t, r);
+}
+
+// Quotient by a divisor fixed for the launch, for numerators below 2^31:
+// with s = ceil(log2 d) and M = ceil(2^(31+s) / d), M - 2^(31+s)/d < 1 and so
+// n M / 2^(31+s) exceeds n/d by less than n / 2^(31+s) <= 1/d: the floor is
+// the same.
+struct FastDiv {
+  uint32_t d, mul, shift;
+  static FastDiv make(uint32_t d) {
+    uint32_t s = 0;
+    while ((1ull << s) < d) ++s;
+    return {d, (uint32_t)(((1ull << (31 + s)) + d - 1) / d), 31 + s};
+  }
+  __host__ __device__ inline uint32_t div(uint32_t n) const {
+    return (uint32_t)(((uint64_t)n * mul) >> shift);
+  }
+};
+
+// A batch as the kernels read it.
+struct Seqs {
+  const int32_t *table;
+  const int32_t *lens;
+  const int32_t *q_start;  // or nullptr: sequence b has row b only
+  uint32_t n_seqs, table_stride, n_tokens, max_len, n_pages;
+  FastDiv page;
+
+  // rows [row, row + n) are the sequence's new tokens, clamped to the batch
+  __host__ __device__ inline void rows(uint32_t b, uint32_t &row, uint32_t &n) const {
+    if (q_start == nullptr) {
+      row = b;
+      n = 1;
+      return;
+    }
+    const int32_t a = q_start[b], e = q_start[b + 1];
+    const int32_t lim = (int32_t)n_tokens;
+    row = (uint32_t)(a < 0 ? 0 : a > lim ? lim : a);
+    const uint32_t end = (uint32_t)(e < 0 ? 0 : e > lim ? lim : e);
+    n = end > row ? end - row : 0;
+  }
+  __host__ __device__ inline bool rows_bad(uint32_t b) const {
+    return q_start != nullptr &&
+           (q_start[b] < 0 || q_start[b + 1] < q_start[b] || q_start[b + 1] > (int32_t)n_tokens);
+  }
+  // the length, within [0, max_len]
+  __host__ __device__ inline int32_t len(uint32_t b) const {
+    const int32_t m = lens[b];
+    return m < 0 ? 0 : m > (int32_t)max_len ? (int32_t)max_len : m;
+  }
+  __host__ __device__ inline bool len_bad(uint32_t b) const {
+    return lens[b] < 0 || lens[b] > (int32_t)max_len;
+  }
+};
+
+// Slot (token row of the pool) of token j, 0 <= j < max_len, of the sequence
+// with page ids `table`.  False for an id outside the pool; the slot is then
+// one inside it, so that a caller that goes on reads nothing out of bounds.
+__host__ __device__ inline bool slot_of(const int32_t *table, const FastDiv &page,
+                                        uint32_t n_pages, uint32_t j, uint32_t &slot) {
+  const uint32_t e = page.div(j);
+  uint32_t id = (uint32_t)table[e];
+  const bool ok = id < n_pages;
+  if (!ok) id = 0;
+  slot = id * page.d + (j - e * page.d);
+  return ok;
+}
+
+hipError_t launch_append(const kvc_paged_desc &p, const Seqs &s, uint32_t layer, void *pool,
+                         const void *k, uint64_t k_stride, const void *v, uint64_t v_stride,
+                         const void *q, uint64_t q_stride, void *q_out, uint64_t q_out_stride,
+                         const kvc_rope *rope, int32_t *status, hipStream_t stream);
+hipError_t launch_page_copy(const kvc_paged_desc &p, void *pool, const int32_t *table,
+                            uint32_t first_token, uint32_t n_tokens, void *flat, uint32_t T_total,
+                            uint32_t flat_first, bool out, int32_t *status, hipStream_t stream);
+
+// One attention call.
+struct AttendArgs {
+  Seqs s;
+  const void *k, *v;  // the layer's keys and values: [n_pages * page_tokens][C]
+  uint64_t row;       // elements from one cached token to the next (C)
+  const void *q;
+  uint64_t q_stride;
+  void *out;
+  uint64_t out_stride;
+  float *lse;
+  float *part;      // [tiles][n_kv_heads][splits][16][head_dim] binary32
+  float *part_ml;   // [tiles][n_kv_heads][splits][2][16]
+  uint32_t n_heads, n_kv_heads, group;
+  uint32_t tiles;   // row tiles launched
+  uint32_t splits;
+  float scale;      // scale * log2(e)
+  uint32_t window;
+  int32_t *status;
+};
+uint64_t attend_ws_bytes(const kvc_paged_desc &p, const kvc_paged_batch &b);
+hipError_t launch_attend(const kvc_paged_desc &p, const kvc_paged_batch &b, AttendArgs a, void *ws,
+                         hipStream_t stream);
+
+}  // namespace kvc
