@@ -15,6 +15,7 @@ namespace {
 
 typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // D = A B + C on 16 x 16 tiles over 32 products.  Lane l holds of A row l%16
 // and of B column l%16, products (l/16)*8 .. +7 of both; of C and D column
@@ -29,6 +30,26 @@ __device__ inline f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
+// The same on 32 x 32 tiles over 16 products: lane l holds of A row l%32 and
+// of B column l%32, products (l/32)*8 .. +7; of C and D column l%32 and, as
+// element i, row (i/4)*8 + (l/32)*4 + i%4.
+template <class T>
+__device__ inline f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+  if constexpr (std::is_same<T, f16>::value)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// Combines lanes l and l ^ 32.
+__device__ inline float other_half(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __builtin_bit_cast(float, (threadIdx.x & 32) ? r[0] : r[1]);
+}
+
 constexpr float kLn2 = 0.69314718055994530942f;
 __device__ inline float ninf() { return -__builtin_inff(); }
 
@@ -40,11 +61,33 @@ __device__ inline float ninf() { return -__builtin_inff(); }
 // probability instead of 2^-24, so a long tail of small ones is not lost.
 template <class T>
 constexpr float kShift = std::is_same<T, f16>::value ? 14.0f : 0.0f;
+// In the kernel of 128 rows a probability may pass 1 by 2^kGrow before the
+// sums are rescaled, and binary16 holds less than 2^16.
+constexpr float kGrow = 4.0f;
+template <class T>
+constexpr float kShiftBig = std::is_same<T, f16>::value ? 11.0f : 0.0f;
+template <class T, uint32_t kRows>
+constexpr float kShiftOf = kRows == 16 ? kShift<T> : kShiftBig<T>;
+
+// The scale's sign goes into the queries, and a scale of 0 makes them 0 (with
+// a scale of 1), so that the kernels multiply by a positive number: the
+// largest product then has the largest score, and a hidden token's -infinity
+// stays one.
+struct Scale {
+  uint32_t q_and, q_xor;
+  float s;
+};
+__device__ inline Scale scale_of(float s) {
+  return {s == 0.0f ? 0u : 0xFFFFFFFFu, s < 0.0f ? 0x80008000u : 0u,
+          s == 0.0f ? 1.0f : __builtin_fabsf(s)};
+}
 
 // 8 consecutive elements of a query row in the cache's type.
 template <class TI, class TC>
-__device__ inline u32x4 load_q8(const TI *p) {
+__device__ inline u32x4 load_q8(const TI *p, const Scale &sc) {
   u32x4 w = load16(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = (w[i] & sc.q_and) ^ sc.q_xor;
   if constexpr (!std::is_same<TI, TC>::value) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = pack2<TC>(elem_lo<TI>(w[i]), elem_hi<TI>(w[i]));
@@ -80,6 +123,15 @@ __device__ inline Words<N> load_words(const void *p) {
     r.w[1] = v[1];
   }
   return r;
+}
+
+// The transposing LDS read: in each group of 16 lanes, lane 4r + c names 8
+// bytes (elements 4c .. 4c+3 of row r), and lane i receives element i of rows
+// 0 .. 3.
+__device__ inline u32x2 read_tr(const uint8_t *p) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                       (__attribute__((address_space(3))) s16x4 *)p));
 }
 
 // A dword holds two elements: is either an infinity or NaN?
@@ -202,6 +254,7 @@ __global__ __launch_bounds__(256) void k_attend_rows(AttendArgs a) {
   const int32_t t_lo = (int32_t)((int64_t)n_tiles * split / a.splits);
   const int32_t t_hi = (int32_t)((int64_t)n_tiles * (split + 1) / a.splits);
   const uint32_t qh = hk * a.group + row.head;
+  const Scale sc_q = scale_of(a.scale);
 
   u32x4 qf[KK];
 #pragma unroll
@@ -210,7 +263,7 @@ __global__ __launch_bounds__(256) void k_attend_rows(AttendArgs a) {
     const TI *q = static_cast<const TI *>(a.q) + (uint64_t)row.token * a.q_stride +
                   (uint64_t)qh * D + g4 * 8;
 #pragma unroll
-    for (int kk = 0; kk < KK; ++kk) qf[kk] = load_q8<TI, TC>(q + kk * 32);
+    for (int kk = 0; kk < KK; ++kk) qf[kk] = load_q8<TI, TC>(q + kk * 32, sc_q);
   }
 
   float m = ninf(), l = 0.0f;
@@ -259,7 +312,7 @@ __global__ __launch_bounds__(256) void k_attend_rows(AttendArgs a) {
     }
     float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = sc[i >> 2][i & 3] * a.scale;
+    for (int i = 0; i < 8; ++i) x[i] = sc[i >> 2][i & 3] * sc_q.s;
     // some token of the tile is hidden from some row
     const bool edge = j0 < r_last.lo || j0 + (int32_t)kTok > r_first.hi;
     if (edge) {
@@ -421,29 +474,312 @@ __global__ __launch_bounds__(256) void k_attend_rows(AttendArgs a) {
   }
 }
 
-// Joins the splits of a row: a wave per (row tile, KV head, row).
+// ------------------------------------------------------ 128 rows a workgroup
+// For prompts: four waves of 32 rows each share tiles of 64 tokens in LDS (32
+// where head_dim is 256), so
+// a key or value is fetched once for 128 rows.  Scores are transposed here
+// too (S^T = K Q^T on 32 x 32 tiles): a lane holds half a row's scores, the
+// other half of the row in lane ^ 32, so a row's maximum is a chain in one
+// lane and one exchange, and P^T is again the second operand of O^T = V^T P^T
+// without leaving its lane.  V^T comes from LDS through the transposing read,
+// four tokens of a dimension at a time.
+//
+// Tiles are double-buffered: the next one is loaded to registers while this
+// one is multiplied, then stored to the other buffer: one barrier a tile.
+// Rows of K are padded by 16 bytes, so that 16-byte reads of eight rows (or
+// sixteen) fall into different banks, rows of V by 32, so that the four rows
+// of a transposing read do.
+//
+// The sums are rescaled only when some row of the wave grew by more than
+// kGrow binary orders since its reference was set.
+constexpr uint32_t kBigRows = 128;
+template <int D>
+constexpr uint32_t kBigTok = D == 256 ? 32 : 64;  // 32: a tile's registers would not fit
+template <int D>
+constexpr uint32_t kKeyStride = D * 2 + 16;
+template <int D>
+constexpr uint32_t kValStride = D * 2 + 32;
+template <int D>
+constexpr uint32_t kBigBuf = kBigTok<D> * (kKeyStride<D> + kValStride<D>);
+template <int D>
+constexpr uint32_t kBigLds = 2 * kBigBuf<D> + 32;
+
 template <class TI, class TC, int D>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_tile(AttendArgs a) {
+  constexpr int TOK = kBigTok<D>, HT = TOK / 32;
+  constexpr int KK = D / 16;        // steps of the first product
+  constexpr int DT = D / 32;        // dimension tiles of the second
+  constexpr int CH = D / 8;         // 16-byte vectors of a row
+  constexpr int NC = CH * TOK / 256;  // of them each thread moves
+  extern __shared__ __align__(16) uint8_t lds[];
+  uint32_t *s_odd = reinterpret_cast<uint32_t *>(lds + 2 * kBigBuf<D>);  // [3][2]
+  const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const uint32_t n32 = lane & 31, hi = lane >> 5;
+  const uint32_t hk = blockIdx.x % a.n_kv_heads;
+  const uint32_t rest = blockIdx.x / a.n_kv_heads;
+  const uint32_t split = rest % a.splits, tile = rest / a.splits;
+  Tile t;
+  if (!find_tile<kBigRows>(a, tile, t)) return;
+  const int32_t len = a.s.len(t.b);
+  if (threadIdx.x == 0 && a.s.len_bad(t.b)) set_status(a.status, KVC_ERR_SHAPE);
+  const uint32_t w0 = wave * 32;
+  const bool busy = w0 < t.rows;  // the wave has rows
+  const bool live = w0 + n32 < t.rows;
+  const Row row = row_of(a, t, len, t.first + (live ? w0 + n32 : 0));
+  const Row r_first = row_of(a, t, len, t.first), r_last = row_of(a, t, len, t.first + t.rows - 1);
+  const Row w_first = row_of(a, t, len, t.first + (busy ? w0 : 0));
+  const Row w_last = row_of(a, t, len, t.first + (busy ? min(w0 + 31, t.rows - 1) : 0));
+  const int32_t begin = r_first.lo, end = r_last.hi, last = end - 1;
+  const int32_t n_tiles = end > begin ? (end - begin + TOK - 1) / TOK : 0;
+  const int32_t t_lo = (int32_t)((int64_t)n_tiles * split / a.splits);
+  const int32_t t_hi = (int32_t)((int64_t)n_tiles * (split + 1) / a.splits);
+  const uint32_t qh = hk * a.group + row.head;
+  const Scale sc_q = scale_of(a.scale);
+
+  u32x4 qf[KK];
+#pragma unroll
+  for (int kk = 0; kk < KK; ++kk) qf[kk] = u32x4{0, 0, 0, 0};
+  if (live) {
+    const TI *q = static_cast<const TI *>(a.q) + (uint64_t)row.token * a.q_stride +
+                  (uint64_t)qh * D + hi * 8;
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) qf[kk] = load_q8<TI, TC>(q + kk * 16, sc_q);
+  }
+  float ref = ninf(), l = 0.0f;
+  f32x16 o[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+
+  const int32_t *table = a.s.table + (uint64_t)t.b * a.s.table_stride;
+  const TC *kbase = static_cast<const TC *>(a.k) + (uint64_t)hk * D;
+  const TC *vbase = static_cast<const TC *>(a.v) + (uint64_t)hk * D;
+  bool bad = false;
+
+  // this thread's vectors of a tile: token st_t[i], vector st_c[i]
+  u32x4 kr[NC], vr[NC];
+  uint32_t slot[NC];
+  auto find_slots = [&](int32_t ti) {
+    const int32_t j0 = begin + ti * TOK;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      int32_t j = j0 + (int32_t)((threadIdx.x + 256 * i) / CH);
+      j = j < last ? j : last;
+      bad = !slot_of(table, a.s.page, a.s.n_pages, (uint32_t)j, slot[i]) || bad;
+    }
+  };
+  auto load_tile = [&]() {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const uint32_t c = (threadIdx.x + 256 * i) % CH;
+      kr[i] = load16(kbase + (uint64_t)slot[i] * a.row + c * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const uint32_t c = (threadIdx.x + 256 * i) % CH;
+      vr[i] = load16(vbase + (uint64_t)slot[i] * a.row + c * 8);
+    }
+  };
+  // Hidden tokens of a value tile must not meet the second product with an
+  // infinity or NaN (0 times it is NaN): tokens past the end are zeroed, and
+  // a token that some rows see and others do not is noted in s_odd.
+  auto store_tile = [&](int32_t ti, uint32_t odd_at) {
+    const int32_t j0 = begin + ti * TOK;
+    uint8_t *kb = lds + (ti & 1) * kBigBuf<D>, *vb = kb + TOK * kKeyStride<D>;
+    if (j0 < r_last.lo || j0 + TOK > r_first.hi) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const uint32_t jt = (threadIdx.x + 256 * i) / CH;
+        if (j0 + (int32_t)jt >= end) vr[i] = u32x4{0, 0, 0, 0};
+        bool nf = false;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) nf = nf || nonfinite2<TC>(vr[i][w]);
+        if (nf) atomicOr(&s_odd[odd_at * 2 + (jt >> 5)], 1u << (jt & 31));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const uint32_t jt = (threadIdx.x + 256 * i) / CH, c = (threadIdx.x + 256 * i) % CH;
+      store16(kb + jt * kKeyStride<D> + c * 16, kr[i]);
+      store16(vb + jt * kValStride<D> + c * 16, vr[i]);
+    }
+  };
+
+  if (threadIdx.x < 6) s_odd[threadIdx.x] = 0;
+  uint32_t odd_at = 0;  // of the tile being multiplied: its number mod 3
+  if (t_lo < t_hi) {
+    find_slots(t_lo);
+    load_tile();
+    if (t_lo + 1 < t_hi) find_slots(t_lo + 1);
+    __syncthreads();  // s_odd is zero
+    store_tile(t_lo, 0);
+    __syncthreads();
+  }
+  for (int32_t ti = t_lo; ti < t_hi; ++ti) {
+    const int32_t j0 = begin + ti * TOK;
+    uint8_t *kb = lds + (ti & 1) * kBigBuf<D>, *vb = kb + TOK * kKeyStride<D>;
+    const bool more = ti + 1 < t_hi;
+    if (more) load_tile();
+    if (ti + 2 < t_hi) find_slots(ti + 2);
+    const uint32_t next_odd = odd_at == 2 ? 0 : odd_at + 1;
+    uint64_t odd = 0;
+    // the slot that tile ti + 2 will use: last read a barrier ago
+    if (threadIdx.x < 2) s_odd[(next_odd == 2 ? 0 : next_odd + 1) * 2 + threadIdx.x] = 0;
+    if (j0 < r_last.lo || j0 + TOK > r_first.hi) {
+      odd = s_odd[odd_at * 2] | (uint64_t)s_odd[odd_at * 2 + 1] << 32;
+      if (odd) {
+        __syncthreads();  // every wave has read the mask
+        for (uint32_t i = threadIdx.x; i < (uint32_t)(TOK * CH); i += 256)
+          if ((odd >> (i / CH)) & 1)
+            store16(vb + (i / CH) * kValStride<D> + (i % CH) * 16, u32x4{0, 0, 0, 0});
+        __syncthreads();
+      }
+    }
+    // a wave has nothing to do where none of its rows sees a token
+    if (busy && j0 < w_last.hi && j0 + TOK > w_first.lo) {
+      f32x16 s[HT];
+#pragma unroll
+      for (int h = 0; h < HT; ++h) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[h][i] = 0.0f;
+        const uint8_t *kp = kb + (h * 32 + n32) * kKeyStride<D> + hi * 16;
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) s[h] = mfma32<TC>(load16(kp + kk * 32), qf[kk], s[h]);
+      }
+      if (j0 < w_last.lo || j0 + TOK > w_first.hi) {
+#pragma unroll
+        for (int h = 0; h < HT; ++h)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int32_t j = j0 + h * 32 + (i >> 2) * 8 + (int32_t)hi * 4 + (i & 3);
+            s[h][i] = j >= row.lo && j < row.hi ? s[h][i] : ninf();
+          }
+      }
+      float mt = s[0][0];
+#pragma unroll
+      for (int i = 1; i < HT * 16; ++i) mt = __builtin_fmaxf(mt, s[i >> 4][i & 15]);
+      mt = __builtin_fmaxf(mt, other_half(mt)) * sc_q.s;
+      if (__any(mt > ref + kGrow)) {
+        const float nr = __builtin_fmaxf(ref, mt);
+        const float alpha = nr == ninf() ? 1.0f : __builtin_amdgcn_exp2f(ref - nr);
+        ref = nr;
+        l *= alpha;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d] *= alpha;
+      }
+      const float off = kShiftBig<TC> - (ref == ninf() ? 0.0f : ref);
+      float sum = 0.0f;
+#pragma unroll
+      for (int h = 0; h < HT; ++h)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          s[h][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[h][i], sc_q.s, off));
+          sum += s[h][i];
+        }
+      l += sum;
+      // tokens noted in s_odd: added lane by lane where the row sees them
+      for (uint64_t left = odd; left; left &= left - 1) {
+        const uint32_t jt = (uint32_t)__builtin_ctzll(left), e = jt & 31;
+        const uint32_t at = (jt >> 5) * 16 + (e >> 3) * 4 + (e & 3);
+        float pj = 0.0f;
+#pragma unroll
+        for (int i = 0; i < HT * 16; ++i) pj = at == (uint32_t)i ? s[i >> 4][i & 15] : pj;
+        pj = __shfl(pj, (int)(n32 + 32 * ((e >> 2) & 1)));
+        const int32_t j = j0 + (int32_t)jt;
+        uint32_t sj;
+        slot_of(table, a.s.page, a.s.n_pages, (uint32_t)(j < last ? j : last), sj);
+        if (j >= row.lo && j < row.hi) {
+          const TC *vp = vbase + (uint64_t)sj * a.row + hi * 4;
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              o[d][i] = __builtin_fmaf(pj, (float)vp[d * 32 + (i >> 2) * 8 + (i & 3)], o[d][i]);
+        }
+      }
+      // lane l reads token (l%16)/4 (+ 4 for the upper half), dimensions
+      // (l/16%2)*16 + (l%4)*4 .. +3 and receives four tokens of dimension l%32
+      const uint8_t *vp = vb + (hi * 4 + ((lane & 15) >> 2)) * kValStride<D> +
+                          ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+#pragma unroll
+      for (int st = 0; st < TOK / 16; ++st) {
+        u32x4 pf;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          pf[i] = pack2<TC>(s[st >> 1][(st & 1) * 8 + 2 * i], s[st >> 1][(st & 1) * 8 + 2 * i + 1]);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          const uint8_t *p0 = vp + st * 16 * kValStride<D> + d * 64;
+          const u32x2 v0 = read_tr(p0), v1 = read_tr(p0 + 8 * kValStride<D>);
+          o[d] = mfma32<TC>(u32x4{v0[0], v0[1], v1[0], v1[1]}, pf, o[d]);
+        }
+      }
+    }
+    if (more) store_tile(ti + 1, next_odd);
+    odd_at = next_odd;
+    __syncthreads();
+  }
+  if (__ballot(bad) && lane == 0) set_status(a.status, KVC_ERR_SHAPE);
+  l += other_half(l);
+  if (!live) return;
+  if (a.splits == 1) {
+    const bool some = row.hi > row.lo;
+    const float inv = some ? 1.0f / l : 0.0f;
+    TI *op = static_cast<TI *>(a.out) + (uint64_t)row.token * a.out_stride + (uint64_t)qh * D +
+             hi * 4;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        u32x2 w;
+        w[0] = some ? pack2<TI>(o[d][4 * i] * inv, o[d][4 * i + 1] * inv) : 0u;
+        w[1] = some ? pack2<TI>(o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv) : 0u;
+        *reinterpret_cast<u32x2 *>(op + d * 32 + i * 8) = w;
+      }
+    if (hi == 0 && a.lse)
+      a.lse[(uint64_t)row.token * a.n_heads + qh] =
+          some ? (ref - kShiftBig<TC> + __builtin_amdgcn_logf(l)) * kLn2 : ninf();
+  } else {
+    const uint64_t part = ((uint64_t)tile * a.n_kv_heads + hk) * a.splits + split;
+    float *op = a.part + (part * kBigRows + w0 + n32) * D + hi * 4;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<f32x4 *>(op + d * 32 + i * 8) =
+            f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+    if (hi == 0) {
+      a.part_ml[part * (2 * kBigRows) + w0 + n32] = ref;
+      a.part_ml[part * (2 * kBigRows) + kBigRows + w0 + n32] = l;
+    }
+  }
+}
+
+// Joins the splits of a row: a wave per (row tile, KV head, row).
+template <class TI, class TC, int D, uint32_t kRows>
 __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
   const uint32_t lane = threadIdx.x & 63;
-  const uint32_t unit = blockIdx.x / 4, r = (blockIdx.x % 4) * 4 + (threadIdx.x >> 6);
+  const uint32_t unit = blockIdx.x / (kRows / 4);
+  const uint32_t r = (blockIdx.x % (kRows / 4)) * 4 + (threadIdx.x >> 6);
   const uint32_t hk = unit % a.n_kv_heads, tile = unit / a.n_kv_heads;
   Tile t;
-  if (!find_tile<16>(a, tile, t)) return;
+  if (!find_tile<kRows>(a, tile, t)) return;
   if (r >= t.rows) return;
   const Row row = row_of(a, t, a.s.len(t.b), t.first + r);
   const uint64_t part = ((uint64_t)tile * a.n_kv_heads + hk) * a.splits;
   float mm = ninf();
   for (uint32_t s = lane; s < a.splits; s += 64)
-    mm = __builtin_fmaxf(mm, a.part_ml[(part + s) * 32 + r]);
+    mm = __builtin_fmaxf(mm, a.part_ml[(part + s) * (2 * kRows) + r]);
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) mm = __builtin_fmaxf(mm, __shfl_xor(mm, d));
   const float ref = mm == ninf() ? 0.0f : mm;
   float acc[(D + 127) / 128 * 2] = {};
   float l = 0.0f;
   for (uint32_t s = 0; s < a.splits; ++s) {
-    const float f = __builtin_amdgcn_exp2f(a.part_ml[(part + s) * 32 + r] - ref);
-    l = __builtin_fmaf(a.part_ml[(part + s) * 32 + 16 + r], f, l);
-    const float *op = a.part + ((part + s) * 16 + r) * D;
+    const float f = __builtin_amdgcn_exp2f(a.part_ml[(part + s) * (2 * kRows) + r] - ref);
+    l = __builtin_fmaf(a.part_ml[(part + s) * (2 * kRows) + kRows + r], f, l);
+    const float *op = a.part + ((part + s) * kRows + r) * D;
 #pragma unroll
     for (int k = 0; k < (D + 127) / 128; ++k) {
       const uint32_t dim = (lane + 64 * k) * 2;
@@ -466,54 +802,66 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
   }
   if (lane == 0 && a.lse)
     a.lse[(uint64_t)row.token * a.n_heads + h] =
-        some ? (mm - kShift<TC> + __builtin_amdgcn_logf(l)) * kLn2 : ninf();
+        some ? (mm - kShiftOf<TC, kRows> + __builtin_amdgcn_logf(l)) * kLn2 : ninf();
 }
 
 // ------------------------------------------------------------------- host
 struct Plan {
-  uint32_t tiles, splits;
+  uint32_t rows, tiles, splits;
   uint64_t part, part_ml, total;  // workspace offsets
 };
 
 Plan make_plan(const kvc_paged_desc &p, const kvc_paged_batch &b) {
   Plan w{};
   const uint32_t group = p.n_heads / p.n_kv_heads;
+  // 128-row tiles once the sequences have as many rows to a KV head on average
+  w.rows = b.q_start && (uint64_t)b.n_tokens * group >= (uint64_t)b.n_seqs * 128 ? 128 : 16;
   // every sequence's last tile may be partly filled
-  w.tiles = b.q_start ? (uint32_t)((uint64_t)b.n_tokens * group / 16) +
+  w.tiles = b.q_start ? (uint32_t)((uint64_t)b.n_tokens * group / w.rows) +
                             std::min(b.n_seqs, b.n_tokens)
                       : b.n_seqs * ((group + 15) / 16);
   const uint64_t units = (uint64_t)w.tiles * p.n_kv_heads;
-  // enough workgroups for the 256 CUs, three to each, but at least 256
+  // enough workgroups for the 256 CUs, two or three to each, but at least 256
   // tokens to a split
-  const uint64_t want = (3 * 256 + units - 1) / std::max<uint64_t>(units, 1);
+  const uint64_t fill = (w.rows == 16 ? 3 : 2) * 256;
+  const uint64_t want = (fill + units - 1) / std::max<uint64_t>(units, 1);
   w.splits = (uint32_t)std::max<uint64_t>(
       1, std::min<uint64_t>(want, ((uint64_t)b.max_len + 255) / 256));
   if (w.splits > 1) {
     const uint64_t n = units * w.splits;
-    w.part_ml = n * 16 * p.head_dim * 4;
-    w.total = w.part_ml + n * 32 * 4;
+    w.part_ml = n * w.rows * p.head_dim * 4;
+    w.total = w.part_ml + n * w.rows * 2 * 4;
     w.total = (w.total + 255) & ~uint64_t(255);
   }
   return w;
 }
 
 template <class TI, class TC, int D>
-hipError_t launch_d(const kvc_paged_desc &p, const AttendArgs &a, hipStream_t stream) {
+hipError_t launch_d(const AttendArgs &a, uint32_t rows, hipStream_t stream) {
   const uint32_t units = a.tiles * a.n_kv_heads;
-  hipLaunchKernelGGL((k_attend_rows<TI, TC, D>), dim3(units * a.splits), dim3(256), 0,
-                     stream, a);
-  if (a.splits > 1)
-    hipLaunchKernelGGL((k_attend_join<TI, TC, D>), dim3(units * 4), dim3(256), 0, stream, a);
+  if (rows == 16) {
+    hipLaunchKernelGGL((k_attend_rows<TI, TC, D>), dim3(units * a.splits), dim3(256), 0, stream,
+                       a);
+    if (a.splits > 1)
+      hipLaunchKernelGGL((k_attend_join<TI, TC, D, 16>), dim3(units * 4), dim3(256), 0, stream, a);
+  } else {
+    hipLaunchKernelGGL((k_attend_tile<TI, TC, D>), dim3(units * a.splits), dim3(256), kBigLds<D>,
+                       stream, a);
+    if (a.splits > 1)
+      hipLaunchKernelGGL((k_attend_join<TI, TC, D, 128>), dim3(units * 32), dim3(256), 0, stream,
+                         a);
+  }
   return hipGetLastError();
 }
 
 template <class TI, class TC>
-hipError_t launch_t(const kvc_paged_desc &p, const AttendArgs &a, hipStream_t stream) {
+hipError_t launch_t(const kvc_paged_desc &p, const AttendArgs &a, uint32_t rows,
+                    hipStream_t stream) {
   switch (p.head_dim) {
-    case 64: return launch_d<TI, TC, 64>(p, a, stream);
-    case 96: return launch_d<TI, TC, 96>(p, a, stream);
-    case 128: return launch_d<TI, TC, 128>(p, a, stream);
-    default: return launch_d<TI, TC, 256>(p, a, stream);
+    case 64: return launch_d<TI, TC, 64>(a, rows, stream);
+    case 96: return launch_d<TI, TC, 96>(a, rows, stream);
+    case 128: return launch_d<TI, TC, 128>(a, rows, stream);
+    default: return launch_d<TI, TC, 256>(a, rows, stream);
   }
 }
 
@@ -531,9 +879,9 @@ hipError_t launch_attend(const kvc_paged_desc &p, const kvc_paged_batch &b, Atte
   uint8_t *base = static_cast<uint8_t *>(ws);
   a.part = reinterpret_cast<float *>(base + w.part);
   a.part_ml = reinterpret_cast<float *>(base + w.part_ml);
-  if (p.io_dtype == KVC_F16) return launch_t<f16, f16>(p, a, stream);
-  if (p.cache_dtype == KVC_BF16) return launch_t<bf16, bf16>(p, a, stream);
-  return launch_t<bf16, f16>(p, a, stream);
+  if (p.io_dtype == KVC_F16) return launch_t<f16, f16>(p, a, w.rows, stream);
+  if (p.cache_dtype == KVC_BF16) return launch_t<bf16, bf16>(p, a, w.rows, stream);
+  return launch_t<bf16, f16>(p, a, w.rows, stream);
 }
 
 }  // namespace kvc

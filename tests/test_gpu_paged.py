@@ -141,6 +141,14 @@ PROMPT = [
     (3, 3, 256, 64, F16, F16, [200], [131], 1),
     (6, 6, 64, 1, F16, F16, [70, 3, 65], [70, 0, 64], 7),
     (64, 1, 64, 32, BF16, F16, [129], [9], 0),
+    # 128-row tiles: a split context, no grouping, a group of 7 and of 128, windows
+    (8, 2, 128, 16, F16, F16, [2050], [40], 0),
+    (2, 2, 128, 64, BF16, BF16, [257, 700], [257, 129], 0),
+    (7, 1, 128, 20, BF16, F16, [333, 0, 90], [333, 0, 3], 100),
+    (128, 1, 64, 16, F16, F16, [70, 5], [3, 5], 0),
+    (8, 1, 96, 48, BF16, BF16, [1300], [33], 700),
+    (4, 1, 256, 16, F16, F16, [530], [64], 0),
+    (6, 2, 64, 7, F16, F16, [64, 128, 127], [64, 64, 127], 65),
 ]
 
 
@@ -167,12 +175,13 @@ def test_attend_padding_rows():
     _check_attend(st, out, lse)
 
 
+@pytest.mark.parametrize("heads", [2, 8])
 @pytest.mark.parametrize("dtype", [F16, BF16])
-def test_attend_nonfinite_hidden_values(dtype):
+def test_attend_nonfinite_hidden_values(dtype, heads):
     """Infinities and NaN in the cached rows of tokens that a row does not
     see (later tokens of the same prompt, tokens before its window) have no
     effect on that row."""
-    st = Setup([90, 64], [60, 64], 8, 2, 64, 16, dtype, dtype, spare=1)
+    st = Setup([90, 64], [60, 64], heads, 2, 64, 16, dtype, dtype, spare=1)
     window = 24
     bad = [(0, 80), (0, 45), (1, 63), (1, 20)]
     for b, t in bad:
