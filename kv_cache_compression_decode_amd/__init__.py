@@ -899,27 +899,31 @@ class Rope:
 
 
 def _pool_ptr(desc: PagedDesc, pool: torch.Tensor, device) -> int:
-    if tuple(pool.shape) != desc.pool_shape or pool.device != device:
-        raise ValueError(f"the pool must have shape {desc.pool_shape} and the batch's device")
+    if pool.shape != desc.pool_shape or pool.device != device or not pool.is_contiguous():
+        raise ValueError(f"the pool must be contiguous, of shape {desc.pool_shape}, on the "
+                         "batch's device")
     if pool.dtype != torch.int16 and pool.dtype != _DTYPES[desc.cache_dtype]:
         raise ValueError("the pool's type differs from the descriptor's")
-    return _kv_ptr(pool)
+    return pool.data_ptr()
 
 
-def _token_rows(t: torch.Tensor, n: int, heads: int, desc: PagedDesc, device, what: str) -> int:
+def _token_rows(t: torch.Tensor, n: int, heads: int, dim: int, dtype, device, what: str) -> int:
     """Checks [n][heads][head_dim] rows and returns their token stride."""
     s = t.stride()
-    if (tuple(t.shape) != (n, heads, desc.head_dim) or t.dtype != _DTYPES[desc.io_dtype]
-            or t.device != device or s[2] != 1 or (heads > 1 and s[1] != desc.head_dim)):
-        raise ValueError(f"{what} must be [{n}][{heads}][{desc.head_dim}] rows of the "
-                         "descriptor's io type on the batch's device, each row contiguous")
-    return s[0] if n > 1 else heads * desc.head_dim
+    if (t.shape != (n, heads, dim) or t.dtype != dtype or t.device != device or s[2] != 1
+            or (heads > 1 and s[1] != dim)):
+        raise ValueError(f"{what} must be [{n}][{heads}][{dim}] rows of the descriptor's io type "
+                         "on the batch's device, each row contiguous")
+    return s[0] if n > 1 else heads * dim
 
 
-def _paged_stream(stream: Optional[torch.cuda.Stream], device) -> ctypes.c_void_p:
-    if device.index != torch.cuda.current_device():
+def _paged_stream(stream: Optional[torch.cuda.Stream], device):
+    """_stream for a step's many small calls: the current stream's handle
+    without a Stream object."""
+    index = device.index
+    if index != torch._C._cuda_getDevice():
         raise ValueError("the tensors' device must be the current one")
-    return _stream(stream)
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
 
 
 def append_async(desc: PagedDesc, batch: PagedBatch, layer: int, pool: torch.Tensor,
@@ -931,18 +935,19 @@ def append_async(desc: PagedDesc, batch: PagedBatch, layer: int, pool: torch.Ten
     turned by rope (no sync; device errors stay in wsp.status)."""
     dev = batch.device
     n = k.shape[0]
-    b = batch._args(desc, n)
-    ks = _token_rows(k, n, desc.n_kv_heads, desc, dev, "k")
-    vs = _token_rows(v, n, desc.n_kv_heads, desc, dev, "v")
+    heads, dim, dtype = desc.n_kv_heads, desc.head_dim, _DTYPES[desc.io_dtype]
+    ks = _token_rows(k, n, heads, dim, dtype, dev, "k")
+    vs = _token_rows(v, n, heads, dim, dtype, dev, "v")
     qs = os_ = 0
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     if q is not None:
-        qs = _token_rows(q, n, desc.n_heads, desc, dev, "q")
-        os_ = _token_rows(q_out, n, desc.n_heads, desc, dev, "q_out")
+        heads = desc.n_heads
+        qs = _token_rows(q, n, heads, dim, dtype, dev, "q")
+        os_ = _token_rows(q_out, n, heads, dim, dtype, dev, "q_out")
     if rope is not None and rope.cos_sin.device != dev:
         raise ValueError("the rotation table must be on the batch's device")
-    _check(lib().kvc_append(desc, b, layer, _pool_ptr(desc, pool, dev), k.data_ptr(), ks,
+    _check(lib().kvc_append(desc, batch._args(desc, n), layer, _pool_ptr(desc, pool, dev), k.data_ptr(), ks,
                             v.data_ptr(), vs, None if q is None else q.data_ptr(), qs,
                             None if q is None else q_out.data_ptr(), os_,
                             None if rope is None else rope._args(), wsp.status.data_ptr(),
@@ -953,18 +958,18 @@ def _attend(name: str, desc: PagedDesc, batch: PagedBatch, layer: int, pool, q, 
             window, lse, stream) -> None:
     dev = batch.device
     n = q.shape[0]
-    b = batch._args(desc, n)
-    qs = _token_rows(q, n, desc.n_heads, desc, dev, "q")
-    os_ = _token_rows(out, n, desc.n_heads, desc, dev, "out")
-    if lse is not None and (tuple(lse.shape) != (n, desc.n_heads) or lse.device != dev
+    heads, dim, dtype = desc.n_heads, desc.head_dim, _DTYPES[desc.io_dtype]
+    qs = _token_rows(q, n, heads, dim, dtype, dev, "q")
+    os_ = _token_rows(out, n, heads, dim, dtype, dev, "out")
+    if lse is not None and (lse.shape != (n, heads) or lse.device != dev
                             or lse.dtype != torch.float32 or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous [n_tokens][n_heads] float32 tensor")
     if window < 0:
         raise ValueError("window must not be negative")
     if wsp.ws.device != dev:
         raise ValueError("the workspace must be on the batch's device")
-    _check(getattr(lib(), name)(desc, b, layer, _pool_ptr(desc, pool, dev), q.data_ptr(), qs,
-                                desc.head_dim ** -0.5 if scale is None else scale, window,
+    _check(getattr(lib(), name)(desc, batch._args(desc, n), layer, _pool_ptr(desc, pool, dev),
+                                q.data_ptr(), qs, dim ** -0.5 if scale is None else scale, window,
                                 out.data_ptr(), os_, None if lse is None else lse.data_ptr(),
                                 wsp.ws.data_ptr(), wsp.ws_bytes, wsp.status.data_ptr(),
                                 _paged_stream(stream, dev)), name)
@@ -994,7 +999,7 @@ def _page_args(desc: PagedDesc, pool, table, flat, status):
     _int32_tensor(table, 1, "table")
     _int32_tensor(status, 1, "status")
     shape = (desc.n_layers, 2, flat.shape[2], desc.n_kv_heads * desc.head_dim)
-    if tuple(flat.shape) != shape or any(t.device != dev for t in (table, flat, status)):
+    if flat.shape != shape or table.device != dev or flat.device != dev or status.device != dev:
         raise ValueError(f"the tensor must have shape {shape} and the pool's device")
     return dev, _pool_ptr(desc, pool, dev), _kv_ptr(flat)
 

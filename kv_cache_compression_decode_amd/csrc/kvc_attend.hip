@@ -66,8 +66,6 @@ constexpr float kShift = std::is_same<T, f16>::value ? 14.0f : 0.0f;
 constexpr float kGrow = 4.0f;
 template <class T>
 constexpr float kShiftBig = std::is_same<T, f16>::value ? 11.0f : 0.0f;
-template <class T, uint32_t kRows>
-constexpr float kShiftOf = kRows == 16 ? kShift<T> : kShiftBig<T>;
 
 // The scale's sign goes into the queries, and a scale of 0 makes them 0 (with
 // a scale of 1), so that the kernels multiply by a positive number: the
@@ -142,59 +140,11 @@ __device__ inline bool nonfinite2(uint32_t w) {
 }
 
 // ------------------------------------------------------------ row tiles
-// Row tile `t` of the launch: rows [first, first + rows) of sequence b, in
-// sequence order, every sequence's rows cut into tiles of kRows.
+// Rows [first, first + rows) of sequence b.
 struct Tile {
   uint32_t b, row0, n;  // the sequence, its first token row and token count
   uint32_t first, rows;
 };
-
-// Each wave finds the tile by itself: 64 sequences at a time, a scan of
-// their tile counts.  False if the batch has fewer tiles.
-template <uint32_t kRows>
-__device__ inline bool find_tile(const AttendArgs &a, uint32_t t, Tile &out) {
-  const uint32_t lane = threadIdx.x & 63;
-  if (a.s.q_start == nullptr) {  // one token each: the same number of tiles for all
-    const uint32_t per = (a.group + kRows - 1) / kRows;
-    out.b = t / per;
-    if (out.b >= a.s.n_seqs) return false;
-    out.row0 = out.b;
-    out.n = 1;
-    out.first = (t - out.b * per) * kRows;
-    out.rows = min(kRows, a.group - out.first);
-    return true;
-  }
-  uint32_t base = 0;
-  for (uint32_t b0 = 0; b0 < a.s.n_seqs; b0 += 64) {
-    uint32_t row0 = 0, n = 0;
-    const uint32_t b = b0 + lane;
-    if (b < a.s.n_seqs) {
-      a.s.rows(b, row0, n);
-      if (t == 0 && a.s.rows_bad(b)) set_status(a.status, KVC_ERR_SHAPE);
-    }
-    const uint32_t mine = (n * a.group + kRows - 1) / kRows;
-    uint32_t sum = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const uint32_t o = __shfl_up(sum, d);
-      if (lane >= (uint32_t)d) sum += o;
-    }
-    const uint64_t above = __ballot(base + sum > t);
-    if (above) {
-      const int src = __builtin_ctzll(above);
-      out.b = b0 + (uint32_t)src;
-      out.row0 = __shfl(row0, src);
-      out.n = __shfl(n, src);
-      const uint32_t k = t - base - __shfl(sum - mine, src);
-      out.first = k * kRows;
-      if (out.first >= out.n * a.group) return false;  // only if q_start overlaps itself
-      out.rows = min(kRows, out.n * a.group - out.first);
-      return true;
-    }
-    base += __shfl(sum, 63);
-  }
-  return false;
-}
 
 // Where a row writes, and its visible tokens [lo, hi).
 struct Row {
@@ -203,7 +153,7 @@ struct Row {
 };
 __device__ inline Row row_of(const AttendArgs &a, const Tile &t, int32_t len, uint32_t r) {
   Row w;
-  const uint32_t i = r / a.group;
+  const uint32_t i = a.group_div.div(r);
   w.head = r - i * a.group;
   w.token = t.row0 + i;
   const int32_t pos = len - (int32_t)t.n + (int32_t)i;
@@ -212,11 +162,130 @@ __device__ inline Row row_of(const AttendArgs &a, const Tile &t, int32_t len, ui
   return w;
 }
 
+// ---------------------------------------------------- sharing out the tokens
+// The work of a call is a line of steps (one tile of 32 tokens for one row
+// tile and KV head): head by head, in each the row tiles in sequence order,
+// in each its tokens.  The line is cut into equal pieces, one to a workgroup,
+// wherever the cuts fall, so workgroups finish together however uneven the
+// lengths are.  A workgroup that holds all of a row tile's steps writes its
+// rows' outputs; one that holds a part writes its sums, maxima and
+// unnormalised output to the workspace (at most two parts, at its piece's two
+// ends) and k_attend_join adds them up.  All heads have the same row tiles,
+// so the workgroups of different heads run over the same tokens at the same
+// time, and their short rows (head_dim elements) make up whole cached tokens.
+//
+// Where no cache is longer than a few steps (`whole`), every row tile counts
+// as one step, is never cut, and needs no join.
+constexpr uint32_t kRowTile = 16;
+constexpr uint32_t kTok = 32;
+
+struct Work {
+  uint32_t b, k;   // the sequence and its row tile
+  uint32_t row0, n, tiles;  // its token rows and row tiles
+  int32_t len;
+
+  // steps of row tile k of a sequence: at least one, so that every row is written
+  __device__ static uint32_t steps_of(const AttendArgs &a, uint32_t n, int32_t len, uint32_t k) {
+    if (a.whole) return 1;
+    const uint32_t first = k * kRowTile, last = min(first + kRowTile, n * a.group) - 1;
+    const int32_t p0 = len - (int32_t)n + (int32_t)a.group_div.div(first);
+    const int32_t p1 = len - (int32_t)n + (int32_t)a.group_div.div(last);
+    const int32_t hi = p1 < 0 ? 0 : p1 + 1;
+    const int32_t h0 = p0 < 0 ? 0 : p0 + 1;
+    const int32_t lo = a.window != 0 && (uint32_t)h0 > a.window ? h0 - (int32_t)a.window : 0;
+    const uint32_t s = hi > lo ? ((uint32_t)(hi - lo) + kTok - 1) / kTok : 0;
+    return s ? s : 1;
+  }
+  __device__ static uint32_t tiles_of(const AttendArgs &a, uint32_t n) {
+    return (n * a.group + kRowTile - 1) / kRowTile;
+  }
+  __device__ static uint64_t seq_steps(const AttendArgs &a, uint32_t b) {
+    uint32_t row0, n;
+    a.s.rows(b, row0, n);
+    const uint32_t tiles = tiles_of(a, n);
+    if (a.whole) return tiles;
+    const int32_t len = a.s.len(b);
+    if (n == 1) return (uint64_t)tiles * steps_of(a, 1, len, 0);
+    uint64_t sum = 0;
+    for (uint32_t k = 0; k < tiles; ++k) sum += steps_of(a, n, len, k);
+    return sum;
+  }
+  __device__ void load(const AttendArgs &a, uint32_t seq) {
+    b = seq;
+    a.s.rows(b, row0, n);
+    tiles = tiles_of(a, n);
+    len = a.s.len(b);
+  }
+  __device__ uint32_t steps(const AttendArgs &a) const { return steps_of(a, n, len, k); }
+  // the next row tile; after the last sequence's, the first one's (next head)
+  __device__ void next(const AttendArgs &a, uint32_t &head) {
+    if (++k < tiles) return;
+    k = 0;
+    uint32_t s = b;
+    do {
+      if (++s == a.s.n_seqs) {
+        s = 0;
+        ++head;
+      }
+      load(a, s);
+    } while (tiles == 0);
+  }
+};
+
+// 256 sequences' steps at a time, four to a lane.
+__device__ inline uint64_t shfl64(uint64_t x, int src) {
+  return (uint64_t)__shfl((uint32_t)x, src) | (uint64_t)__shfl((uint32_t)(x >> 32), src) << 32;
+}
+struct Steps {
+  uint64_t w[4], upto;  // the lane's sequences; inclusive sum over the lanes
+  __device__ void load(const AttendArgs &a, uint32_t b0, bool check) {
+    const uint32_t lane = threadIdx.x & 63;
+    upto = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t b = b0 + lane * 4 + i;
+      w[i] = 0;
+      if (b < a.s.n_seqs) {
+        w[i] = Work::seq_steps(a, b);
+        if (check && (a.s.rows_bad(b) || a.s.len_bad(b))) set_status(a.status, KVC_ERR_SHAPE);
+      }
+      upto += w[i];
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint64_t o = shfl64(upto, (int)(lane >= (uint32_t)d ? lane - d : lane));
+      if (lane >= (uint32_t)d) upto += o;
+    }
+  }
+};
+
+// A 64-bit quotient, in 32 bits where both fit.
+__device__ inline uint64_t quot(uint64_t n, uint64_t d) {
+  if (((n | d) >> 32) == 0) return (uint32_t)n / (uint32_t)d;
+  return n / d;
+}
+
+// Piece w of `parts` equal pieces of `total` steps: the first total % parts
+// pieces are one longer.
+struct Pieces {
+  uint64_t per, rem;
+  uint32_t parts;
+  __device__ uint64_t start(uint32_t w) const { return w * per + min((uint64_t)w, rem); }
+  __device__ uint32_t owner(uint64_t x) const {
+    const uint64_t edge = rem * (per + 1);
+    return (uint32_t)(x < edge ? quot(x, per + 1) : rem + quot(x - edge, per));
+  }
+};
+
+// What a workgroup leaves for k_attend_join if its last part is the first one
+// of its row tile: which rows, and the workgroups that hold the others.
+struct JoinInfo {
+  uint32_t valid, b, k, head, last, slot, pad[2];
+};
+
 // ------------------------------------------------------- 16 rows a workgroup
 // The four waves of a workgroup share 16 rows and take tiles of 32 tokens in
-// turn; they are joined through LDS at the end.  With `splits` workgroups to
-// a row tile, each takes an equal share of the tokens and writes its sums,
-// maximum and unnormalised output to the workspace for k_attend_join.
+// turn; they are joined through LDS at the end.
 //
 // Scores are computed transposed, S^T = K Q^T: lane l holds row l%16's scores
 // of tokens (l/16)*4 .. +3 of both halves of the tile.  That is the layout in
@@ -227,10 +296,8 @@ __device__ inline Row row_of(const AttendArgs &a, const Tile &t, int32_t len, ui
 // dimensions of its eight tokens (16 lanes cover whole rows, so the loads are
 // contiguous) and the i-th product takes dimension l%16 * E + i, a byte
 // permutation in registers.  Neither K nor V passes through LDS.
-constexpr uint32_t kTok = 32;
-
 template <class TI, class TC, int D>
-__global__ __launch_bounds__(256) void k_attend_rows(AttendArgs a) {
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArgs a) {
   constexpr int E = D / 16;
   constexpr int KK = D / 32;
   constexpr int EC = E < 8 ? E : 8;  // dimensions a lane joins at a time
@@ -238,240 +305,415 @@ __global__ __launch_bounds__(256) void k_attend_rows(AttendArgs a) {
   __shared__ float s_m[4][16], s_l[4][16];
   const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const uint32_t n16 = lane & 15, g4 = lane >> 4;
-  const uint32_t hk = blockIdx.x % a.n_kv_heads;
-  const uint32_t rest = blockIdx.x / a.n_kv_heads;
-  const uint32_t split = rest % a.splits, tile = rest / a.splits;
-  Tile t;
-  if (!find_tile<16>(a, tile, t)) return;
-  const int32_t len = a.s.len(t.b);
-  if (wave == 0 && lane == 0 && a.s.len_bad(t.b)) set_status(a.status, KVC_ERR_SHAPE);
-  // this lane's row, and the tile's token range
-  const bool live = n16 < t.rows;
-  const Row row = row_of(a, t, len, t.first + (live ? n16 : 0));
-  const Row r_first = row_of(a, t, len, t.first), r_last = row_of(a, t, len, t.first + t.rows - 1);
-  const int32_t begin = r_first.lo, end = r_last.hi;  // lo and hi grow with the row
-  const int32_t n_tiles = end > begin ? (end - begin + (int32_t)kTok - 1) / (int32_t)kTok : 0;
-  const int32_t t_lo = (int32_t)((int64_t)n_tiles * split / a.splits);
-  const int32_t t_hi = (int32_t)((int64_t)n_tiles * (split + 1) / a.splits);
-  const uint32_t qh = hk * a.group + row.head;
-  const Scale sc_q = scale_of(a.scale);
 
-  u32x4 qf[KK];
+  // this workgroup's piece of the line, and where it begins
+  Work u;
+  uint32_t hk;
+  uint64_t at, stop, off;  // off: steps of the first row tile before the piece
+  Pieces pc{1, 0, gridDim.x};
+  if (a.s.q_start == nullptr && a.whole) {  // one row tile each: no search
+    const uint32_t per = Work::tiles_of(a, 1);
+    const uint32_t unit = blockIdx.x / a.n_kv_heads;
+    hk = blockIdx.x - unit * a.n_kv_heads;
+    u.load(a, unit / per);
+    u.k = unit - u.b * per;
+    at = off = 0;
+    stop = 1;
+    if (threadIdx.x == 0 && a.s.len_bad(u.b)) set_status(a.status, KVC_ERR_SHAPE);
+  } else {
+    const bool check = blockIdx.x == 0 && wave == 0;
+    Steps st;
+    uint64_t total = 0;
+    for (uint32_t b0 = 0; b0 < a.s.n_seqs; b0 += 256) {
+      st.load(a, b0, check);
+      total += shfl64(st.upto, 63);
+    }
+    const uint64_t line = total * a.n_kv_heads;
+    // at least kMinSteps to a workgroup
+    const uint64_t most = a.whole ? line : (line + a.min_steps - 1) / a.min_steps;
+    pc.parts = (uint32_t)min((uint64_t)gridDim.x, most);
+    if (blockIdx.x >= pc.parts) {
+      if (threadIdx.x == 0 && a.info) static_cast<JoinInfo *>(a.info)[blockIdx.x].valid = 0;
+      return;
+    }
+    pc.per = quot(line, pc.parts);
+    pc.rem = line - pc.per * pc.parts;
+    at = pc.start(blockIdx.x);
+    stop = pc.start(blockIdx.x + 1);
+    hk = (uint32_t)quot(at, total);
+    uint64_t x = at - hk * total;
+    uint64_t base = 0;
+    for (uint32_t b0 = 0;; b0 += 256) {  // some sequence holds step x < total
+      if (b0 >= a.s.n_seqs) return;
+      if (a.s.n_seqs > 256) st.load(a, b0, false);
+      const uint64_t above = __ballot(base + st.upto > x);
+      if (above == 0) {
+        base += shfl64(st.upto, 63);
+        continue;
+      }
+      const int src = __builtin_ctzll(above);
+      uint64_t w[4], before = shfl64(st.upto, src);
 #pragma unroll
-  for (int kk = 0; kk < KK; ++kk) qf[kk] = u32x4{0, 0, 0, 0};
-  if (live) {
-    const TI *q = static_cast<const TI *>(a.q) + (uint64_t)row.token * a.q_stride +
-                  (uint64_t)qh * D + g4 * 8;
+      for (int i = 0; i < 4; ++i) {
+        w[i] = shfl64(st.w[i], src);
+        before -= w[i];
+      }
+      x -= base + before;
+      uint32_t b = b0 + (uint32_t)src * 4;
 #pragma unroll
-    for (int kk = 0; kk < KK; ++kk) qf[kk] = load_q8<TI, TC>(q + kk * 32, sc_q);
+      for (int i = 0; i < 3; ++i)
+        if (b == b0 + (uint32_t)src * 4 + i && x >= w[i]) {
+          x -= w[i];
+          ++b;
+        }
+      u.load(a, b);
+      u.k = 0;
+      if (u.n == 1) {
+        const uint32_t s = u.steps(a);
+        u.k = (uint32_t)quot(x, s);
+        x -= (uint64_t)u.k * s;
+      } else {
+        for (uint32_t s = u.steps(a); x >= s && u.k + 1 < u.tiles; s = u.steps(a)) {
+          x -= s;
+          ++u.k;
+        }
+      }
+      break;
+    }
+    off = x;
   }
-
-  float m = ninf(), l = 0.0f;
-  f32x4 o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = f32x4{0, 0, 0, 0};
-  const int32_t *table = a.s.table + (uint64_t)t.b * a.s.table_stride;
-  const TC *kbase = static_cast<const TC *>(a.k) + (uint64_t)hk * D;
-  const TC *vbase = static_cast<const TC *>(a.v) + (uint64_t)hk * D;
-  const int32_t last = end - 1;
+  const uint64_t piece = at;
+  if (threadIdx.x == 0 && a.info) static_cast<JoinInfo *>(a.info)[blockIdx.x].valid = 0;
+  const Scale sc_q = scale_of(a.scale);
+  const TC *kcache = static_cast<const TC *>(a.k), *vcache = static_cast<const TC *>(a.v);
   bool bad = false;
 
-  for (int32_t ti = t_lo + (int32_t)wave; ti < t_hi; ti += 4) {
-    const int32_t j0 = begin + ti * (int32_t)kTok;
-    // slots of this lane's two key rows and eight value rows
-    uint32_t kslot[2], vslot[8];
-    {
-      // each lane looks up one token of the tile; the others' come by shuffle
-      int32_t j = j0 + (int32_t)(lane & 31);
+  while (at < stop) {
+    // the part of row tile u.k that this workgroup holds: steps [s_lo, s_hi)
+    const uint32_t steps = u.steps(a);
+    const uint32_t left = (uint32_t)min((uint64_t)(steps - (uint32_t)off), stop - at);
+    const Tile t{u.b, u.row0, u.n, u.k * kRowTile, min(kRowTile, u.n * a.group - u.k * kRowTile)};
+    const bool live = n16 < t.rows;
+    const Row row = row_of(a, t, u.len, t.first + (live ? n16 : 0));
+    const Row r_first = row_of(a, t, u.len, t.first);
+    const Row r_last = row_of(a, t, u.len, t.first + t.rows - 1);
+    const int32_t begin = r_first.lo, end = r_last.hi;  // lo and hi grow with the row
+    const int32_t tiles = end > begin ? (int32_t)(((uint32_t)(end - begin) + kTok - 1) / kTok) : 0;
+    const int32_t t_lo = a.whole ? 0 : (int32_t)off;
+    const int32_t t_hi = a.whole ? tiles : min(tiles, (int32_t)((uint32_t)off + left));
+    const uint32_t qh = hk * a.group + row.head;
+
+    u32x4 qf[KK];
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) qf[kk] = u32x4{0, 0, 0, 0};
+    if (live) {
+      const TI *q = static_cast<const TI *>(a.q) + (uint64_t)row.token * a.q_stride +
+                    (uint64_t)qh * D + g4 * 8;
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) qf[kk] = load_q8<TI, TC>(q + kk * 32, sc_q);
+    }
+
+    float m = ninf(), l = 0.0f;
+    f32x4 o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = f32x4{0, 0, 0, 0};
+    const int32_t *table = a.s.table + (uint64_t)t.b * a.s.table_stride;
+    const TC *kbase = kcache + (uint64_t)hk * D, *vbase = vcache + (uint64_t)hk * D;
+    const int32_t last = end - 1;
+    // Each lane looks up one token of a tile (the others' slots come by
+    // shuffle), a tile ahead of its use.
+    uint32_t ahead = 0;
+    auto look_up = [&](int32_t ti) {
+      int32_t j = begin + ti * (int32_t)kTok + (int32_t)(lane & 31);
       j = j < last ? j : last;
-      uint32_t slot;
-      bad = !slot_of(table, a.s.page, a.s.n_pages, (uint32_t)j, slot) || bad;
-      kslot[0] = __shfl(slot, n16);
-      kslot[1] = __shfl(slot, 16 + n16);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) vslot[i] = __shfl(slot, (i >> 2) * 16 + g4 * 4 + (i & 3));
-    }
-    u32x4 kf[2][KK];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const TC *kp = kbase + (uint64_t)kslot[h] * a.row + g4 * 8;
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk) kf[h][kk] = load16(kp + kk * 32);
-    }
-    Words<E / 2> vf[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      vf[i] = load_words<E / 2>(vbase + (uint64_t)vslot[i] * a.row + n16 * E);
+      bad = !slot_of(table, a.s.page, a.s.n_pages, (uint32_t)j, ahead) || bad;
+    };
+    if (t_lo + (int32_t)wave < t_hi) look_up(t_lo + (int32_t)wave);
 
-    f32x4 sc[2];
+    for (int32_t ti = t_lo + (int32_t)wave; ti < t_hi; ti += 4) {
+      const int32_t j0 = begin + ti * (int32_t)kTok;
+      // slots of this lane's two key rows and eight value rows
+      uint32_t kslot[2], vslot[8];
+      kslot[0] = __shfl(ahead, n16);
+      kslot[1] = __shfl(ahead, 16 + n16);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      sc[h] = f32x4{0, 0, 0, 0};
+      for (int i = 0; i < 8; ++i) vslot[i] = __shfl(ahead, (i >> 2) * 16 + g4 * 4 + (i & 3));
+      u32x4 kf[2][KK];
 #pragma unroll
-      for (int kk = 0; kk < KK; ++kk) sc[h] = mfma16<TC>(kf[h][kk], qf[kk], sc[h]);
-    }
-    float x[8];
+      for (int h = 0; h < 2; ++h) {
+        const TC *kp = kbase + (uint64_t)kslot[h] * a.row + g4 * 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = sc[i >> 2][i & 3] * sc_q.s;
-    // some token of the tile is hidden from some row
-    const bool edge = j0 < r_last.lo || j0 + (int32_t)kTok > r_first.hi;
-    if (edge) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int32_t j = j0 + (i >> 2) * 16 + (int32_t)g4 * 4 + (i & 3);
-        x[i] = j >= row.lo && j < row.hi ? x[i] : ninf();
+        for (int kk = 0; kk < KK; ++kk) kf[h][kk] = load16(kp + kk * 32);
       }
-    }
-    float mt = x[0];
+      Words<E / 2> vf[8];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) mt = __builtin_fmaxf(mt, x[i]);
-    mt = __builtin_fmaxf(mt, __shfl_xor(mt, 16));
-    mt = __builtin_fmaxf(mt, __shfl_xor(mt, 32));
-    const float mn = __builtin_fmaxf(m, mt);
-    const float ref = mn == ninf() ? 0.0f : mn;  // nothing visible yet: exp2(-inf - 0) = 0
-    const float alpha = __builtin_amdgcn_exp2f(m - ref);
-    m = mn;
-    float p[8];
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      p[i] = __builtin_amdgcn_exp2f(x[i] - ref + kShift<TC>);
-      sum += p[i];
-    }
-    l = __builtin_fmaf(l, alpha, sum);
-    u32x4 pf;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) pf[i] = pack2<TC>(p[2 * i], p[2 * i + 1]);
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] *= alpha;
+      for (int i = 0; i < 8; ++i)
+        vf[i] = load_words<E / 2>(vbase + (uint64_t)vslot[i] * a.row + n16 * E);
 
-    if (edge) {
-      // A hidden token's probability is 0, but 0 times an infinity or NaN of
-      // its value row is not: tokens hidden from every row are zeroed here,
-      // and a token that some rows see and others do not (its row of V not
-      // finite) is taken out of the product and added lane by lane, where
-      // the row's own visibility decides.
-      bool odd = false;
+      if (ti + 4 < t_hi) look_up(ti + 4);
+
+      f32x4 sc[2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int32_t j = j0 + (i >> 2) * 16 + (int32_t)g4 * 4 + (i & 3);
-        bool nf = false;
+      for (int h = 0; h < 2; ++h) {
+        sc[h] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int w = 0; w < E / 2; ++w) {
-          if (j >= end || j < begin) vf[i].w[w] = 0;
-          nf = nf || nonfinite2<TC>(vf[i].w[w]);
-        }
-        odd = odd || nf;
+        for (int kk = 0; kk < KK; ++kk) sc[h] = mfma16<TC>(kf[h][kk], qf[kk], sc[h]);
       }
-      if (__ballot(odd)) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = sc[i >> 2][i & 3] * sc_q.s;
+      // some token of the tile is hidden from some row
+      const bool edge = j0 < r_last.lo || j0 + (int32_t)kTok > r_first.hi;
+      if (edge) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
+          const int32_t j = j0 + (i >> 2) * 16 + (int32_t)g4 * 4 + (i & 3);
+          x[i] = j >= row.lo && j < row.hi ? x[i] : ninf();
+        }
+      }
+      float mt = x[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) mt = __builtin_fmaxf(mt, x[i]);
+      mt = __builtin_fmaxf(mt, __shfl_xor(mt, 16));
+      mt = __builtin_fmaxf(mt, __shfl_xor(mt, 32));
+      const float mn = __builtin_fmaxf(m, mt);
+      const float ref = mn == ninf() ? 0.0f : mn;  // nothing visible yet: exp2(-inf - 0) = 0
+      const float alpha = __builtin_amdgcn_exp2f(m - ref);
+      m = mn;
+      float p[8];
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(x[i] - ref + kShift<TC>);
+        sum += p[i];
+      }
+      l = __builtin_fmaf(l, alpha, sum);
+      u32x4 pf;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pf[i] = pack2<TC>(p[2 * i], p[2 * i + 1]);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= alpha;
+
+      if (edge) {
+        // A hidden token's probability is 0, but 0 times an infinity or NaN of
+        // its value row is not: tokens hidden from every row are zeroed here,
+        // and a token that some rows see and others do not (its row of V not
+        // finite) is taken out of the product and added lane by lane, where
+        // the row's own visibility decides.
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int32_t j = j0 + (i >> 2) * 16 + (int32_t)g4 * 4 + (i & 3);
           bool nf = false;
 #pragma unroll
-          for (int w = 0; w < E / 2; ++w) nf = nf || nonfinite2<TC>(vf[i].w[w]);
-          const uint64_t who = __ballot(nf);
-          for (uint32_t g = 0; g < 4; ++g) {
-            if (((who >> (16 * g)) & 0xFFFFu) == 0) continue;
-            // token (half, g, i): its probability for this lane's row is in
-            // lane g*16 + n16; its values at this lane's output dimensions
-            const int32_t j = j0 + (i >> 2) * 16 + (int32_t)g * 4 + (i & 3);
-            const float pj = __shfl(p[i], (int)(g * 16 + n16));
-            const uint32_t sj = __shfl(vslot[i], (int)(g * 16));
-            if (g4 == g) {
+          for (int w = 0; w < E / 2; ++w) {
+            if (j >= end || j < begin) vf[i].w[w] = 0;
+            nf = nf || nonfinite2<TC>(vf[i].w[w]);
+          }
+          odd = odd || nf;
+        }
+        if (__ballot(odd)) {
 #pragma unroll
-              for (int w = 0; w < E / 2; ++w) vf[i].w[w] = 0;
-            }
-            if (j >= row.lo && j < row.hi) {
-              const TC *vp = vbase + (uint64_t)sj * a.row;
+          for (int i = 0; i < 8; ++i) {
+            bool nf = false;
 #pragma unroll
-              for (int e = 0; e < E; ++e)
+            for (int w = 0; w < E / 2; ++w) nf = nf || nonfinite2<TC>(vf[i].w[w]);
+            const uint64_t who = __ballot(nf);
+            for (uint32_t g = 0; g < 4; ++g) {
+              if (((who >> (16 * g)) & 0xFFFFu) == 0) continue;
+              // token (half, g, i): its probability for this lane's row is in
+              // lane g*16 + n16; its values at this lane's output dimensions
+              const int32_t j = j0 + (i >> 2) * 16 + (int32_t)g * 4 + (i & 3);
+              const float pj = __shfl(p[i], (int)(g * 16 + n16));
+              const uint32_t sj = __shfl(vslot[i], (int)(g * 16));
+              if (g4 == g) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                  o[e][c] = __builtin_fmaf(pj, (float)vp[(g4 * 4 + c) * E + e], o[e][c]);
+                for (int w = 0; w < E / 2; ++w) vf[i].w[w] = 0;
+              }
+              if (j >= row.lo && j < row.hi) {
+                const TC *vp = vbase + (uint64_t)sj * a.row;
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+#pragma unroll
+                  for (int c = 0; c < 4; ++c)
+                    o[e][c] = __builtin_fmaf(pj, (float)vp[(g4 * 4 + c) * E + e], o[e][c]);
+              }
             }
           }
         }
       }
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        u32x4 vt;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          vt[i] = __builtin_amdgcn_perm(vf[2 * i + 1].w[e / 2], vf[2 * i].w[e / 2],
+                                        (e & 1) ? 0x07060302u : 0x05040100u);
+        o[e] = mfma16<TC>(vt, pf, o[e]);
+      }
+    }
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+
+    // join the waves: each one's sums times exp2(its maximum - the common one)
+    if (lane < 16) {
+      s_m[wave][lane] = m;
+      s_l[wave][lane] = l;
+    }
+    __syncthreads();
+    float mm = ninf(), ll = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) mm = __builtin_fmaxf(mm, s_m[w][n16]);
+    const float mref = mm == ninf() ? 0.0f : mm;
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      ll = __builtin_fmaf(s_l[w][n16], __builtin_amdgcn_exp2f(s_m[w][n16] - mref), ll);
+    const bool some = row.hi > row.lo;
+    const bool single = off == 0 && left == steps;
+    const float f = __builtin_amdgcn_exp2f(m - mref) * (single ? (some ? 1.0f / ll : 0.0f) : 1.0f);
+    const uint32_t slot = at == piece ? 0 : 1;
+    const uint64_t part = (uint64_t)blockIdx.x * 2 + slot;
+    if (wave == 0 && lane < t.rows) {
+      if (!single) {
+        a.part_ml[part * 32 + lane] = mm;
+        a.part_ml[part * 32 + 16 + lane] = ll;
+      } else if (a.lse) {
+        a.lse[(uint64_t)row.token * a.n_heads + qh] =
+            some ? (mm - kShift<TC> + __builtin_amdgcn_logf(ll)) * kLn2 : ninf();
+      }
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      u32x4 vt;
+    for (int e0 = 0; e0 < E; e0 += EC) {
+      if (e0) __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        vt[i] = __builtin_amdgcn_perm(vf[2 * i + 1].w[e / 2], vf[2 * i].w[e / 2],
-                                      (e & 1) ? 0x07060302u : 0x05040100u);
-      o[e] = mfma16<TC>(vt, pf, o[e]);
+      for (int e = 0; e < EC; ++e)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          s_o[wave][n16][(g4 * 4 + c) * EC + e] = o[e0 + e][c] * f;
+      __syncthreads();
+      // 16 rows of 16 * EC dimensions, two at a time; dimension k * E + e0 + e
+      for (uint32_t i = threadIdx.x; i < t.rows * 8u * EC; i += 256) {
+        const uint32_t r = i / (8u * EC), x = (i - r * (8u * EC)) * 2;
+        float v0 = 0.0f, v1 = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          v0 += s_o[w][r][x];
+          v1 += s_o[w][r][x + 1];
+        }
+        const uint32_t dim = E == EC ? x : (x / EC) * E + e0 + x % EC;
+        if (single) {
+          const Row w = row_of(a, t, u.len, t.first + r);
+          uint32_t *op = reinterpret_cast<uint32_t *>(
+              static_cast<TI *>(a.out) + (uint64_t)w.token * a.out_stride +
+              (uint64_t)(hk * a.group + w.head) * D + dim);
+          *op = w.hi > w.lo ? pack2<TI>(v0, v1) : 0u;
+        } else {
+          float *op = a.part + (part * 16 + r) * D + dim;
+          op[0] = v0;
+          op[1] = v1;
+        }
+      }
+    }
+    if (threadIdx.x == 0 && off == 0 && left < steps) {
+      JoinInfo *info = static_cast<JoinInfo *>(a.info) + blockIdx.x;
+      info->b = u.b;
+      info->k = u.k;
+      info->head = hk;
+      info->last = pc.owner(at + steps - 1);
+      info->slot = slot;
+      info->valid = 1;
+    }
+    at += left;
+    off = 0;
+    if (at < stop) {
+      u.next(a, hk);
+      __syncthreads();  // s_m, s_l and s_o are free again
     }
   }
   if (__ballot(bad) && lane == 0) set_status(a.status, KVC_ERR_SHAPE);
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
+}
 
-  // join the waves: each one's sums times exp2(its maximum - the common one)
-  if (lane < 16) {
-    s_m[wave][lane] = m;
-    s_l[wave][lane] = l;
-  }
-  __syncthreads();
-  float mm = ninf();
+// Joins the parts of a row tile that k_attend_rows cut: one workgroup for
+// each of its workgroups, which has work if that one held a row tile's first
+// part and not its last.  16 waves share the rows; the waves of a row share
+// the parts and are added up through LDS in a fixed order.
+template <class TI, class TC, int D>
+__global__ __launch_bounds__(1024) void k_attend_rows_join(AttendArgs a) {
+  constexpr int N = D > 128 ? 4 : D > 64 ? 2 : 1;  // dimensions a lane
+  __shared__ float s_acc[16][D];
+  const JoinInfo info = static_cast<const JoinInfo *>(a.info)[blockIdx.x];
+  if (!info.valid) return;
+  const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  uint32_t row0, n;
+  a.s.rows(info.b, row0, n);
+  const Tile t{info.b, row0, n, info.k * kRowTile, min(kRowTile, n * a.group - info.k * kRowTile)};
+  uint32_t per = 16;  // waves to a row
+  while (per > 1 && per * t.rows > 16) per >>= 1;
+  const uint32_t r = wave / per, sub = wave - r * per;
+  const bool live = r < t.rows;
+  const uint32_t parts = info.last - blockIdx.x + 1;
+  auto part_of = [&](uint32_t i) {
+    return i == 0 ? (uint64_t)blockIdx.x * 2 + info.slot : (uint64_t)(blockIdx.x + i) * 2;
+  };
+  float mm = ninf(), l = 0.0f, acc[N] = {};
+  float ref = 0.0f;
+  const bool mine = lane * N < D;
+  if (live) {
+    for (uint32_t i = lane; i < parts; i += 64)
+      mm = __builtin_fmaxf(mm, a.part_ml[part_of(i) * 32 + r]);
 #pragma unroll
-  for (int w = 0; w < 4; ++w) mm = __builtin_fmaxf(mm, s_m[w][n16]);
-  const float mref = mm == ninf() ? 0.0f : mm;
-  const float f = __builtin_amdgcn_exp2f(m - mref);
-  const bool single = a.splits == 1;
-  const uint64_t part = ((uint64_t)tile * a.n_kv_heads + hk) * a.splits + split;
-#pragma unroll
-  for (int e0 = 0; e0 < E; e0 += EC) {
-    if (e0) __syncthreads();
-#pragma unroll
-    for (int e = 0; e < EC; ++e)
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        s_o[wave][n16][(g4 * 4 + c) * EC + e] = o[e0 + e][c] * f;
-    __syncthreads();
-    // 16 rows of 16 * EC dimensions, two at a time; dimension k * E + e0 + e
-    for (uint32_t i = threadIdx.x; i < 16u * 8u * EC; i += 256) {
-      const uint32_t r = i / (8u * EC), x = (i - r * (8u * EC)) * 2;
-      if (r >= t.rows) continue;
-      float v0 = 0.0f, v1 = 0.0f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        v0 += s_o[w][r][x];
-        v1 += s_o[w][r][x + 1];
+    for (int d = 1; d < 64; d <<= 1) mm = __builtin_fmaxf(mm, __shfl_xor(mm, d));
+    ref = mm == ninf() ? 0.0f : mm;
+    for (uint32_t i0 = 0; i0 < parts; i0 += 64) {
+      float f = 0.0f;
+      if (i0 + lane < parts) {
+        const uint64_t p = part_of(i0 + lane);
+        f = __builtin_amdgcn_exp2f(a.part_ml[p * 32 + r] - ref);
+        l = __builtin_fmaf(a.part_ml[p * 32 + 16 + r], f, l);
       }
-      const uint32_t dim = E == EC ? x : (x / EC) * E + e0 + x % EC;
-      if (single) {
-        float mr = ninf(), lr = 0.0f;
+      const uint32_t here = min(64u, parts - i0);
+      // eight parts' loads in flight; past the last one: the last one times 0
+      for (uint32_t i = sub; i < here; i += 8 * per) {
+        float fi[8], x[8][N];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) mr = __builtin_fmaxf(mr, s_m[w][r]);
-        const float rr = mr == ninf() ? 0.0f : mr;
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t ij = i + j * per, ic = min(ij, here - 1);
+          fi[j] = ij < here ? __shfl(f, (int)ic) : 0.0f;
+          const float *op = a.part + (part_of(i0 + ic) * 16 + r) * D + lane * N;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) lr += s_l[w][r] * __builtin_amdgcn_exp2f(s_m[w][r] - rr);
-        const Row w = row_of(a, t, len, t.first + r);
-        const bool some = w.hi > w.lo;
-        const float inv = some ? 1.0f / lr : 0.0f;
-        const uint32_t h = hk * a.group + w.head;
-        uint32_t *op = reinterpret_cast<uint32_t *>(static_cast<TI *>(a.out) +
-                                                    (uint64_t)w.token * a.out_stride +
-                                                    (uint64_t)h * D + dim);
-        *op = some ? pack2<TI>(v0 * inv, v1 * inv) : 0u;
-        if (x == 0 && e0 == 0 && a.lse)
-          a.lse[(uint64_t)w.token * a.n_heads + h] =
-              some ? (mr - kShift<TC> + __builtin_amdgcn_logf(lr)) * kLn2 : ninf();
-      } else {
-        float *op = a.part + (part * 16 + r) * D + dim;
-        op[0] = v0;
-        op[1] = v1;
+          for (int e = 0; e < N; ++e) x[j][e] = mine ? op[e] : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int e = 0; e < N; ++e)
+            acc[e] = fi[j] == 0.0f ? acc[e] : __builtin_fmaf(x[j][e], fi[j], acc[e]);
       }
     }
-  }
-  if (!single && threadIdx.x < 16) {
-    float lr = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) lr += s_l[w][n16] * __builtin_amdgcn_exp2f(s_m[w][n16] - mref);
-    a.part_ml[part * 32 + n16] = mm;
-    a.part_ml[part * 32 + 16 + n16] = lr;
+    for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
+    if (mine)
+#pragma unroll
+      for (int e = 0; e < N; ++e) s_acc[wave][lane * N + e] = acc[e];
   }
+  __syncthreads();
+  if (!live || sub != 0) return;
+  const Row row = row_of(a, t, a.s.len(info.b), t.first + r);
+  const bool some = row.hi > row.lo;
+  const float inv = some ? 1.0f / l : 0.0f;
+  const uint32_t h = info.head * a.group + row.head;
+  TI *out = static_cast<TI *>(a.out) + (uint64_t)row.token * a.out_stride + (uint64_t)h * D;
+  for (uint32_t x = lane * 2; x < D; x += 128) {
+    float v0 = 0.0f, v1 = 0.0f;
+    for (uint32_t w = 0; w < per; ++w) {
+      v0 += s_acc[wave + w][x];
+      v1 += s_acc[wave + w][x + 1];
+    }
+    *reinterpret_cast<uint32_t *>(out + x) = some ? pack2<TI>(v0 * inv, v1 * inv) : 0u;
+  }
+  if (lane == 0 && a.lse)
+    a.lse[(uint64_t)row.token * a.n_heads + h] =
+        some ? (mm - kShift<TC> + __builtin_amdgcn_logf(l)) * kLn2 : ninf();
 }
 
 // ------------------------------------------------------ 128 rows a workgroup
@@ -504,6 +746,43 @@ constexpr uint32_t kBigBuf = kBigTok<D> * (kKeyStride<D> + kValStride<D>);
 template <int D>
 constexpr uint32_t kBigLds = 2 * kBigBuf<D> + 32;
 
+// Row tile `t` of the call, the sequences' tiles in sequence order.  Each wave
+// finds it by itself: 64 sequences at a time, a scan of their tile counts.
+// False if the batch has fewer tiles.
+__device__ inline bool find_tile(const AttendArgs &a, uint32_t t, Tile &out) {
+  const uint32_t lane = threadIdx.x & 63;
+  uint32_t base = 0;
+  for (uint32_t b0 = 0; b0 < a.s.n_seqs; b0 += 64) {
+    uint32_t row0 = 0, n = 0;
+    const uint32_t b = b0 + lane;
+    if (b < a.s.n_seqs) {
+      a.s.rows(b, row0, n);
+      if (t == 0 && a.s.rows_bad(b)) set_status(a.status, KVC_ERR_SHAPE);
+    }
+    const uint32_t mine = (n * a.group + kBigRows - 1) / kBigRows;
+    uint32_t sum = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t o = __shfl_up(sum, d);
+      if (lane >= (uint32_t)d) sum += o;
+    }
+    const uint64_t above = __ballot(base + sum > t);
+    if (above) {
+      const int src = __builtin_ctzll(above);
+      out.b = b0 + (uint32_t)src;
+      out.row0 = __shfl(row0, src);
+      out.n = __shfl(n, src);
+      const uint32_t k = t - base - __shfl(sum - mine, src);
+      out.first = k * kBigRows;
+      if (out.first >= out.n * a.group) return false;  // only if q_start overlaps itself
+      out.rows = min(kBigRows, out.n * a.group - out.first);
+      return true;
+    }
+    base += __shfl(sum, 63);
+  }
+  return false;
+}
+
 template <class TI, class TC, int D>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_tile(AttendArgs a) {
   constexpr int TOK = kBigTok<D>, HT = TOK / 32;
@@ -519,7 +798,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_tile(AttendArg
   const uint32_t rest = blockIdx.x / a.n_kv_heads;
   const uint32_t split = rest % a.splits, tile = rest / a.splits;
   Tile t;
-  if (!find_tile<kBigRows>(a, tile, t)) return;
+  if (!find_tile(a, tile, t)) return;
   const int32_t len = a.s.len(t.b);
   if (threadIdx.x == 0 && a.s.len_bad(t.b)) set_status(a.status, KVC_ERR_SHAPE);
   const uint32_t w0 = wave * 32;
@@ -756,15 +1035,16 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_tile(AttendArg
   }
 }
 
-// Joins the splits of a row: a wave per (row tile, KV head, row).
-template <class TI, class TC, int D, uint32_t kRows>
-__global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
+// Joins the splits of k_attend_tile: a wave per (row tile, KV head, row).
+template <class TI, class TC, int D>
+__global__ __launch_bounds__(256) void k_attend_tile_join(AttendArgs a) {
+  constexpr uint32_t kRows = kBigRows;
   const uint32_t lane = threadIdx.x & 63;
   const uint32_t unit = blockIdx.x / (kRows / 4);
   const uint32_t r = (blockIdx.x % (kRows / 4)) * 4 + (threadIdx.x >> 6);
   const uint32_t hk = unit % a.n_kv_heads, tile = unit / a.n_kv_heads;
   Tile t;
-  if (!find_tile<kRows>(a, tile, t)) return;
+  if (!find_tile(a, tile, t)) return;
   if (r >= t.rows) return;
   const Row row = row_of(a, t, a.s.len(t.b), t.first + r);
   const uint64_t part = ((uint64_t)tile * a.n_kv_heads + hk) * a.splits;
@@ -776,6 +1056,7 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
   const float ref = mm == ninf() ? 0.0f : mm;
   float acc[(D + 127) / 128 * 2] = {};
   float l = 0.0f;
+#pragma unroll 4
   for (uint32_t s = 0; s < a.splits; ++s) {
     const float f = __builtin_amdgcn_exp2f(a.part_ml[(part + s) * (2 * kRows) + r] - ref);
     l = __builtin_fmaf(a.part_ml[(part + s) * (2 * kRows) + kRows + r], f, l);
@@ -802,18 +1083,32 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
   }
   if (lane == 0 && a.lse)
     a.lse[(uint64_t)row.token * a.n_heads + h] =
-        some ? (mm - kShiftOf<TC, kRows> + __builtin_amdgcn_logf(l)) * kLn2 : ninf();
+        some ? (mm - kShiftBig<TC> + __builtin_amdgcn_logf(l)) * kLn2 : ninf();
 }
 
 // ------------------------------------------------------------------- host
 struct Plan {
-  uint32_t rows, tiles, splits;
-  uint64_t part, part_ml, total;  // workspace offsets
+  uint32_t rows;      // 16 or 128 to a workgroup
+  uint32_t grid;      // workgroups of the 16-row kernel
+  bool whole, join;   // it cuts no row tile; a second launch is needed
+  uint32_t tiles, splits;             // of the 128-row kernel
+  uint64_t part, part_ml, info, total;  // workspace offsets
 };
+
+// Workgroups that the 256 CUs hold at once (by registers).
+constexpr uint32_t kCus = 256;
+constexpr uint32_t resident(uint32_t head_dim) { return (head_dim == 256 ? 1 : 2) * kCus; }
+
+// A 16-row workgroup takes at least this many steps: one for each wave.
+constexpr uint32_t kMinSteps = 4;
+// Caches of at most this many steps are not cut.
+constexpr uint32_t kWholeSteps = 16;
 
 Plan make_plan(const kvc_paged_desc &p, const kvc_paged_batch &b) {
   Plan w{};
+  if (b.n_seqs == 0 || b.n_tokens == 0) return w;
   const uint32_t group = p.n_heads / p.n_kv_heads;
+  const uint32_t slots = resident(p.head_dim);
   // 128-row tiles once the sequences have as many rows to a KV head on average
   w.rows = b.q_start && (uint64_t)b.n_tokens * group >= (uint64_t)b.n_seqs * 128 ? 128 : 16;
   // every sequence's last tile may be partly filled
@@ -821,47 +1116,60 @@ Plan make_plan(const kvc_paged_desc &p, const kvc_paged_batch &b) {
                             std::min(b.n_seqs, b.n_tokens)
                       : b.n_seqs * ((group + 15) / 16);
   const uint64_t units = (uint64_t)w.tiles * p.n_kv_heads;
-  // enough workgroups for the 256 CUs, two or three to each, but at least 256
-  // tokens to a split
-  const uint64_t fill = (w.rows == 16 ? 3 : 2) * 256;
-  const uint64_t want = (fill + units - 1) / std::max<uint64_t>(units, 1);
-  w.splits = (uint32_t)std::max<uint64_t>(
-      1, std::min<uint64_t>(want, ((uint64_t)b.max_len + 255) / 256));
-  if (w.splits > 1) {
-    const uint64_t n = units * w.splits;
-    w.part_ml = n * w.rows * p.head_dim * 4;
-    w.total = w.part_ml + n * w.rows * 2 * 4;
+  uint64_t parts = 0;
+  if (w.rows == 16) {
+    const uint64_t steps = std::max<uint64_t>(1, ((uint64_t)b.max_len + kTok - 1) / kTok);
+    w.whole = steps <= kWholeSteps;
+    if (w.whole) {
+      // each row tile once; a batch of single tokens needs no search for it
+      w.grid = (uint32_t)(b.q_start ? std::min<uint64_t>(units, 4 * slots) : units);
+    } else {
+      w.grid = (uint32_t)std::min<uint64_t>(slots, (units * steps + kMinSteps - 1) / kMinSteps);
+      w.join = true;
+      parts = 2ull * w.grid;
+    }
+  } else {
+    // Equal splits of every row tile: as many as make the workgroups come out
+    // in whole rounds, at least 256 tokens to a split.
+    const uint64_t most = std::max<uint64_t>(1, ((uint64_t)b.max_len + 255) / 256);
+    w.splits = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(slots / units, most));
+    w.join = w.splits > 1;
+    parts = w.join ? units * w.splits : 0;
+  }
+  if (w.join) {
+    w.part_ml = parts * w.rows * p.head_dim * 4;
+    w.info = w.part_ml + parts * w.rows * 2 * 4;
+    w.total = w.info + (w.rows == 16 ? (uint64_t)w.grid * sizeof(JoinInfo) : 0);
     w.total = (w.total + 255) & ~uint64_t(255);
   }
   return w;
 }
 
 template <class TI, class TC, int D>
-hipError_t launch_d(const AttendArgs &a, uint32_t rows, hipStream_t stream) {
-  const uint32_t units = a.tiles * a.n_kv_heads;
-  if (rows == 16) {
-    hipLaunchKernelGGL((k_attend_rows<TI, TC, D>), dim3(units * a.splits), dim3(256), 0, stream,
-                       a);
-    if (a.splits > 1)
-      hipLaunchKernelGGL((k_attend_join<TI, TC, D, 16>), dim3(units * 4), dim3(256), 0, stream, a);
+hipError_t launch_d(const AttendArgs &a, const Plan &w, hipStream_t stream) {
+  const uint32_t units = w.tiles * a.n_kv_heads;
+  if (w.rows == 16) {
+    hipLaunchKernelGGL((k_attend_rows<TI, TC, D>), dim3(w.grid), dim3(256), 0, stream, a);
+    if (w.join)
+      hipLaunchKernelGGL((k_attend_rows_join<TI, TC, D>), dim3(w.grid), dim3(1024), 0, stream, a);
   } else {
-    hipLaunchKernelGGL((k_attend_tile<TI, TC, D>), dim3(units * a.splits), dim3(256), kBigLds<D>,
+    hipLaunchKernelGGL((k_attend_tile<TI, TC, D>), dim3(units * w.splits), dim3(256), kBigLds<D>,
                        stream, a);
-    if (a.splits > 1)
-      hipLaunchKernelGGL((k_attend_join<TI, TC, D, 128>), dim3(units * 32), dim3(256), 0, stream,
-                         a);
+    if (w.join)
+      hipLaunchKernelGGL((k_attend_tile_join<TI, TC, D>), dim3(units * (kBigRows / 4)), dim3(256),
+                         0, stream, a);
   }
   return hipGetLastError();
 }
 
 template <class TI, class TC>
-hipError_t launch_t(const kvc_paged_desc &p, const AttendArgs &a, uint32_t rows,
+hipError_t launch_t(const kvc_paged_desc &p, const AttendArgs &a, const Plan &w,
                     hipStream_t stream) {
   switch (p.head_dim) {
-    case 64: return launch_d<TI, TC, 64>(a, rows, stream);
-    case 96: return launch_d<TI, TC, 96>(a, rows, stream);
-    case 128: return launch_d<TI, TC, 128>(a, rows, stream);
-    default: return launch_d<TI, TC, 256>(a, rows, stream);
+    case 64: return launch_d<TI, TC, 64>(a, w, stream);
+    case 96: return launch_d<TI, TC, 96>(a, w, stream);
+    case 128: return launch_d<TI, TC, 128>(a, w, stream);
+    default: return launch_d<TI, TC, 256>(a, w, stream);
   }
 }
 
@@ -874,14 +1182,16 @@ uint64_t attend_ws_bytes(const kvc_paged_desc &p, const kvc_paged_batch &b) {
 hipError_t launch_attend(const kvc_paged_desc &p, const kvc_paged_batch &b, AttendArgs a, void *ws,
                          hipStream_t stream) {
   const Plan w = make_plan(p, b);
-  a.tiles = w.tiles;
   a.splits = w.splits;
+  a.whole = w.whole;
+  a.min_steps = kMinSteps;
   uint8_t *base = static_cast<uint8_t *>(ws);
   a.part = reinterpret_cast<float *>(base + w.part);
   a.part_ml = reinterpret_cast<float *>(base + w.part_ml);
-  if (p.io_dtype == KVC_F16) return launch_t<f16, f16>(p, a, w.rows, stream);
-  if (p.cache_dtype == KVC_BF16) return launch_t<bf16, bf16>(p, a, w.rows, stream);
-  return launch_t<bf16, f16>(p, a, w.rows, stream);
+  a.info = w.join && w.rows == 16 ? base + w.info : nullptr;
+  if (p.io_dtype == KVC_F16) return launch_t<f16, f16>(p, a, w, stream);
+  if (p.cache_dtype == KVC_BF16) return launch_t<bf16, bf16>(p, a, w, stream);
+  return launch_t<bf16, f16>(p, a, w, stream);
 }
 
 }  // namespace kvc

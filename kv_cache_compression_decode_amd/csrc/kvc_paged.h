@@ -125,11 +125,15 @@ struct AttendArgs {
   void *out;
   uint64_t out_stride;
   float *lse;
-  float *part;      // [tiles][n_kv_heads][splits][16][head_dim] binary32
-  float *part_ml;   // [tiles][n_kv_heads][splits][2][16]
+  // workspace: parts of row tiles, [part][rows][head_dim] unnormalised sums,
+  // [part][2][rows] maxima and sums of probabilities, and what joins them
+  float *part, *part_ml;
+  void *info;
   uint32_t n_heads, n_kv_heads, group;
-  uint32_t tiles;   // row tiles launched
-  uint32_t splits;
+  FastDiv group_div;
+  uint32_t splits;     // of the 128-row kernel
+  uint32_t min_steps;  // of the 16-row kernel: tiles a workgroup takes at least
+  bool whole;          // the 16-row kernel cuts no row tile
   float scale;      // scale * log2(e)
   uint32_t window;
   int32_t *status;

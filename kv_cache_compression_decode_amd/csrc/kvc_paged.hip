@@ -349,6 +349,7 @@ kvc_status attend(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t la
   a.n_heads = p->n_heads;
   a.n_kv_heads = p->n_kv_heads;
   a.group = p->n_heads / p->n_kv_heads;
+  a.group_div = FastDiv::make(a.group);
   a.scale = scale * 1.44269504088896340736f;
   a.window = window;
   a.status = dev_status;

@@ -121,6 +121,11 @@ SINGLE = [
     (5, 5, 256, 7, F16, F16, [90, 301], 1),
     (128, 1, 64, 1500, F16, F16, [1499, 1500, 1501], 1000),
     (17, 1, 64, 8, BF16, BF16, [0, 0, 5], 4),
+    # more sequences than a search step takes, cut at arbitrary places, and not cut
+    (4, 1, 64, 16, F16, F16, [(i * 37) % 23 * 30 + i % 5 for i in range(300)], 0),
+    (6, 3, 64, 10, BF16, BF16, [(i * 13) % 29 * 17 for i in range(520)], 0),
+    (3, 1, 96, 16, F16, F16, [2000] + [0] * 260 + [1500, 1, 600], 900),
+    (20, 1, 128, 16, BF16, F16, [1100, 513, 2300], 0),
 ]
 
 
@@ -141,6 +146,10 @@ PROMPT = [
     (3, 3, 256, 64, F16, F16, [200], [131], 1),
     (6, 6, 64, 1, F16, F16, [70, 3, 65], [70, 0, 64], 7),
     (64, 1, 64, 32, BF16, F16, [129], [9], 0),
+    # 16-row tiles of several tokens, cut, beside sequences without new tokens
+    (8, 2, 64, 16, F16, F16, [900, 1500, 30, 700, 5], [9, 3, 30, 0, 1], 0),
+    (6, 1, 128, 20, BF16, BF16, [1201, 33, 0, 640], [17, 5, 0, 2], 300),
+    (40, 2, 256, 16, BF16, F16, [800, 513], [3, 2], 0),
     # 128-row tiles: a split context, no grouping, a group of 7 and of 128, windows
     (8, 2, 128, 16, F16, F16, [2050], [40], 0),
     (2, 2, 128, 64, BF16, BF16, [257, 700], [257, 129], 0),
@@ -528,8 +537,8 @@ def test_context_restored_extended_and_evicted():
     """The operators as they are used together: a context's containers are
     decoded straight into consecutive pages of a pool and, for a second copy,
     into a tensor that page_in scatters; a question's tokens are appended and
-    attended, then single tokens; both copies agree bit for bit and with the
-    64-bit form; page_out hands the context back and encode accepts it, its
+    attended, then single tokens; both copies agree with the 64-bit form and,
+    each called by itself, bit for bit; page_out hands the context back and encode accepts it, its
     containers equal to those of the same tokens in a tensor of their own."""
     L, hk, d, heads, page, T = 2, 2, 64, 8, 16, 3100
     g = _gen(9)
@@ -577,15 +586,28 @@ def test_context_restored_extended_and_evicted():
                              rows[:, heads + hk:], wsp, rope=rope, q=rows[:, :heads], q_out=q)
             attend(pd, batch, layer, pool, q, out, wsp, lse=lse)
             kvc.read_status(wsp.status, "step")
-            assert torch.equal(out[:n], out[n:]) and torch.equal(lse[:n], lse[n:])
+            # each copy by itself: the same bits wherever its pages lie
+            alone = []
+            for b in range(2):
+                qs = None if n == 1 else torch.tensor([0, n], dtype=torch.int32, device=DEV)
+                one_batch = kvc.PagedBatch(table[b:b + 1], lens[b:b + 1], q_start=qs,
+                                           max_len=total)
+                one_ws = kvc.PagedWorkspace(pd, one_batch, n)
+                o1, e1 = torch.empty_like(out[:n]), torch.empty_like(lse[:n])
+                attend(pd, one_batch, layer, pool, q[b * n:(b + 1) * n], o1, one_ws, lse=e1)
+                kvc.read_status(one_ws.status, "alone")
+                alone.append((o1, e1))
+            assert torch.equal(alone[0][0], alone[1][0])
+            assert torch.equal(alone[0][1], alone[1][1])
             s = ref.slots(table[1], done, page, DEV)
             k = pool[layer, 0, s].view(-1, hk, d)
             v = pool[layer, 1, s].view(-1, hk, d)
             assert torch.equal(pool[layer, 0, s[:T]], flat[layer, 0].view(F16))
             o, e, bo, be = ref.attend(q[:n], k, v, list(range(done - n, done)), d ** -0.5, 0, F16,
                                       BF16)
-            assert bool(((out[:n].double() - o).abs() <= bo).all())
-            assert bool(((lse[:n].double() - e).abs() <= be).all())
+            for got, got_e in ((out[:n], lse[:n]), (out[n:], lse[n:]), alone[0]):
+                assert bool(((got.double() - o).abs() <= bo).all())
+                assert bool(((got_e.double() - e).abs() <= be).all())
     # evicted again: both copies give the same containers
     blobs = []
     for b in range(2):

@@ -163,6 +163,11 @@ def test_page_refusals(L, name):
 def test_empty_calls_do_nothing(L):
     none = _batch(n_seqs=0, n_tokens=0, table=None, lens=None)
     assert _append(L, b=none) == 0 and _attend(L, b=none) == 0
+    for q_start in (None, A):
+        for n in (0, 3):
+            b = _batch(n_seqs=n, n_tokens=0, q_start=q_start)
+            assert L.kvc_attend_ws_bytes(_desc(), b) == 0
+    assert _attend(L, b=_batch(q_start=A, n_tokens=0), name="kvc_attend_prompt") == 0
     assert _page(L, n=0) == 0 and _page(L, n=0, name="kvc_page_in") == 0
 
 
