@@ -163,8 +163,8 @@ __device__ inline Row row_of(const AttendArgs &a, const Tile &t, int32_t len, ui
 }
 
 // ---------------------------------------------------- sharing out the tokens
-// The work of a call is a line of steps (one tile of 32 tokens for one row
-// tile and KV head): head by head, in each the row tiles in sequence order,
+// The work of a call is a line of steps (a tile of 32 tokens for one row tile
+// and KV head; more tiles where a call's steps would pass 31 bits): head by head, in each the row tiles in sequence order,
 // in each its tokens.  The line is cut into equal pieces, one to a workgroup,
 // wherever the cuts fall, so workgroups finish together however uneven the
 // lengths are.  A workgroup that holds all of a row tile's steps writes its
@@ -179,40 +179,34 @@ __device__ inline Row row_of(const AttendArgs &a, const Tile &t, int32_t len, ui
 constexpr uint32_t kRowTile = 16;
 constexpr uint32_t kTok = 32;
 
+// kOne: one new token a sequence (q_start is NULL).
+template <bool kOne>
 struct Work {
-  uint32_t b, k;   // the sequence and its row tile
+  uint32_t b, k;            // the sequence and its row tile
   uint32_t row0, n, tiles;  // its token rows and row tiles
   int32_t len;
 
   // steps of row tile k of a sequence: at least one, so that every row is written
   __device__ static uint32_t steps_of(const AttendArgs &a, uint32_t n, int32_t len, uint32_t k) {
     if (a.whole) return 1;
-    const uint32_t first = k * kRowTile, last = min(first + kRowTile, n * a.group) - 1;
-    const int32_t p0 = len - (int32_t)n + (int32_t)a.group_div.div(first);
-    const int32_t p1 = len - (int32_t)n + (int32_t)a.group_div.div(last);
-    const int32_t hi = p1 < 0 ? 0 : p1 + 1;
-    const int32_t h0 = p0 < 0 ? 0 : p0 + 1;
+    int32_t h0 = len, hi = len;  // one past the first and the last row's position
+    if (!kOne) {
+      const uint32_t first = k * kRowTile, last = min(first + kRowTile, n * a.group) - 1;
+      const int32_t base = len - (int32_t)n + 1;
+      h0 = max(base + (int32_t)a.group_div.div(first), 0);
+      hi = max(base + (int32_t)a.group_div.div(last), 0);
+    }
     const int32_t lo = a.window != 0 && (uint32_t)h0 > a.window ? h0 - (int32_t)a.window : 0;
-    const uint32_t s = hi > lo ? ((uint32_t)(hi - lo) + kTok - 1) / kTok : 0;
-    return s ? s : 1;
+    return (hi > lo ? ((uint32_t)(hi - lo) - 1) >> a.step_shift : 0) + 1;
   }
   __device__ static uint32_t tiles_of(const AttendArgs &a, uint32_t n) {
     return (n * a.group + kRowTile - 1) / kRowTile;
   }
-  __device__ static uint64_t seq_steps(const AttendArgs &a, uint32_t b) {
-    uint32_t row0, n;
-    a.s.rows(b, row0, n);
-    const uint32_t tiles = tiles_of(a, n);
-    if (a.whole) return tiles;
-    const int32_t len = a.s.len(b);
-    if (n == 1) return (uint64_t)tiles * steps_of(a, 1, len, 0);
-    uint64_t sum = 0;
-    for (uint32_t k = 0; k < tiles; ++k) sum += steps_of(a, n, len, k);
-    return sum;
-  }
   __device__ void load(const AttendArgs &a, uint32_t seq) {
     b = seq;
-    a.s.rows(b, row0, n);
+    row0 = seq;
+    n = 1;
+    if (!kOne) a.s.rows(b, row0, n);
     tiles = tiles_of(a, n);
     len = a.s.len(b);
   }
@@ -228,59 +222,80 @@ struct Work {
         ++head;
       }
       load(a, s);
-    } while (tiles == 0);
+    } while (!kOne && tiles == 0);
   }
 };
 
-// 256 sequences' steps at a time, four to a lane.
-__device__ inline uint64_t shfl64(uint64_t x, int src) {
-  return (uint64_t)__shfl((uint32_t)x, src) | (uint64_t)__shfl((uint32_t)(x >> 32), src) << 32;
+// Inclusive sum over the wave's lanes (DPP: within rows of 16 lanes, then each
+// row's last lane into the rows above).
+__device__ inline uint32_t wave_sums(uint32_t x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);
+  return x;
 }
+
+// 256 sequences' steps at a time, four to a lane (their loads in flight
+// together).
+template <bool kOne>
 struct Steps {
-  uint64_t w[4], upto;  // the lane's sequences; inclusive sum over the lanes
+  uint32_t w[4], upto;  // the lane's sequences; inclusive sum over the lanes
   __device__ void load(const AttendArgs &a, uint32_t b0, bool check) {
     const uint32_t lane = threadIdx.x & 63;
-    upto = 0;
+    int32_t len[4];
+    uint32_t row0[4], n[4];
+    bool odd = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t b = b0 + lane * 4 + i;
-      w[i] = 0;
-      if (b < a.s.n_seqs) {
-        w[i] = Work::seq_steps(a, b);
-        if (check && (a.s.rows_bad(b) || a.s.len_bad(b))) set_status(a.status, KVC_ERR_SHAPE);
+      const uint32_t b = min(b0 + lane * 4 + i, a.s.n_seqs - 1);
+      len[i] = a.s.lens[b];
+      n[i] = 1;
+      if (!kOne) {
+        a.s.rows(b, row0[i], n[i]);
+        odd = odd || a.s.rows_bad(b);
       }
-      upto += w[i];
     }
+    uint32_t sum = 0;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const uint64_t o = shfl64(upto, (int)(lane >= (uint32_t)d ? lane - d : lane));
-      if (lane >= (uint32_t)d) upto += o;
+    for (int i = 0; i < 4; ++i) {
+      odd = odd || a.s.len_out(len[i]);
+      const int32_t m = a.s.clamp_len(len[i]);
+      const uint32_t tiles = Work<kOne>::tiles_of(a, n[i]);
+      uint32_t steps = 0;
+      if (kOne || a.whole) {
+        steps = tiles * (a.whole ? 1 : Work<kOne>::steps_of(a, 1, m, 0));
+      } else {
+        for (uint32_t k = 0; k < tiles; ++k) steps += Work<kOne>::steps_of(a, n[i], m, k);
+      }
+      w[i] = b0 + lane * 4 + i < a.s.n_seqs ? steps : 0;
+      sum += w[i];
     }
+    if (check && odd) set_status(a.status, KVC_ERR_SHAPE);
+    upto = wave_sums(sum);
   }
 };
 
-// A 64-bit quotient, in 32 bits where both fit.
-__device__ inline uint64_t quot(uint64_t n, uint64_t d) {
-  if (((n | d) >> 32) == 0) return (uint32_t)n / (uint32_t)d;
-  return n / d;
-}
-
-// Piece w of `parts` equal pieces of `total` steps: the first total % parts
-// pieces are one longer.
+// Piece w of `parts` equal pieces of the line: the first `rem` pieces are one
+// step longer.
 struct Pieces {
-  uint64_t per, rem;
-  uint32_t parts;
-  __device__ uint64_t start(uint32_t w) const { return w * per + min((uint64_t)w, rem); }
-  __device__ uint32_t owner(uint64_t x) const {
-    const uint64_t edge = rem * (per + 1);
-    return (uint32_t)(x < edge ? quot(x, per + 1) : rem + quot(x - edge, per));
+  uint32_t parts, per, rem;
+  __device__ uint32_t start(uint32_t w) const { return w * per + min(w, rem); }
+  __device__ uint32_t owner(uint32_t x) const {
+    const uint32_t edge = rem * (per + 1);
+    return x < edge ? x / (per + 1) : rem + (x - edge) / per;
   }
 };
 
-// What a workgroup leaves for k_attend_join if its last part is the first one
-// of its row tile: which rows, and the workgroups that hold the others.
+// What the workgroup that holds a row tile's first part leaves for the join:
+// whether there are others, and which workgroups hold them.  One for each
+// workgroup (whose last part alone can be cut and the first of its row tile),
+// or, where single tokens have fewer row tiles than that, one for each row
+// tile and KV head (`by_unit`), so that the join launches no idle workgroups.
 struct JoinInfo {
-  uint32_t valid, b, k, head, last, slot, pad[2];
+  uint32_t cut, b, k, head, first, last, slot, pad;
 };
 
 // ------------------------------------------------------- 16 rows a workgroup
@@ -296,7 +311,7 @@ struct JoinInfo {
 // dimensions of its eight tokens (16 lanes cover whole rows, so the loads are
 // contiguous) and the i-th product takes dimension l%16 * E + i, a byte
 // permutation in registers.  Neither K nor V passes through LDS.
-template <class TI, class TC, int D>
+template <class TI, class TC, int D, bool kOne>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArgs a) {
   constexpr int E = D / 16;
   constexpr int KK = D / 32;
@@ -307,12 +322,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
   const uint32_t n16 = lane & 15, g4 = lane >> 4;
 
   // this workgroup's piece of the line, and where it begins
-  Work u;
+  Work<kOne> u;
   uint32_t hk;
-  uint64_t at, stop, off;  // off: steps of the first row tile before the piece
-  Pieces pc{1, 0, gridDim.x};
-  if (a.s.q_start == nullptr && a.whole) {  // one row tile each: no search
-    const uint32_t per = Work::tiles_of(a, 1);
+  uint32_t at, stop, off;  // off: steps of the first row tile before the piece
+  Pieces pc{gridDim.x, 1, 0};
+  JoinInfo *info = static_cast<JoinInfo *>(a.info);
+  const uint32_t per = Work<kOne>::tiles_of(a, 1);  // row tiles of a single token
+  if (kOne && a.whole) {  // a row tile to a workgroup: no search
     const uint32_t unit = blockIdx.x / a.n_kv_heads;
     hk = blockIdx.x - unit * a.n_kv_heads;
     u.load(a, unit / per);
@@ -321,41 +337,39 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
     stop = 1;
     if (threadIdx.x == 0 && a.s.len_bad(u.b)) set_status(a.status, KVC_ERR_SHAPE);
   } else {
+    const bool by_unit = kOne && a.by_unit;
+    if (!by_unit && threadIdx.x == 0 && info) info[blockIdx.x].cut = 0;
     const bool check = blockIdx.x == 0 && wave == 0;
-    Steps st;
-    uint64_t total = 0;
+    Steps<kOne> st;
+    uint32_t total = 0;
     for (uint32_t b0 = 0; b0 < a.s.n_seqs; b0 += 256) {
       st.load(a, b0, check);
-      total += shfl64(st.upto, 63);
+      total += __builtin_amdgcn_readlane(st.upto, 63);
     }
-    const uint64_t line = total * a.n_kv_heads;
-    // at least kMinSteps to a workgroup
-    const uint64_t most = a.whole ? line : (line + a.min_steps - 1) / a.min_steps;
-    pc.parts = (uint32_t)min((uint64_t)gridDim.x, most);
-    if (blockIdx.x >= pc.parts) {
-      if (threadIdx.x == 0 && a.info) static_cast<JoinInfo *>(a.info)[blockIdx.x].valid = 0;
-      return;
-    }
-    pc.per = quot(line, pc.parts);
+    const uint32_t line = total * a.n_kv_heads;
+    // at least min_steps to a workgroup
+    pc.parts = min(gridDim.x, a.whole ? line : (line + a.min_steps - 1) / a.min_steps);
+    if (blockIdx.x >= pc.parts) return;
+    pc.per = line / pc.parts;
     pc.rem = line - pc.per * pc.parts;
     at = pc.start(blockIdx.x);
     stop = pc.start(blockIdx.x + 1);
-    hk = (uint32_t)quot(at, total);
-    uint64_t x = at - hk * total;
-    uint64_t base = 0;
+    hk = at / total;
+    uint32_t x = at - hk * total;
+    uint32_t base = 0;
     for (uint32_t b0 = 0;; b0 += 256) {  // some sequence holds step x < total
       if (b0 >= a.s.n_seqs) return;
       if (a.s.n_seqs > 256) st.load(a, b0, false);
       const uint64_t above = __ballot(base + st.upto > x);
       if (above == 0) {
-        base += shfl64(st.upto, 63);
+        base += __builtin_amdgcn_readlane(st.upto, 63);
         continue;
       }
       const int src = __builtin_ctzll(above);
-      uint64_t w[4], before = shfl64(st.upto, src);
+      uint32_t w[4], before = __builtin_amdgcn_readlane(st.upto, src);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        w[i] = shfl64(st.w[i], src);
+        w[i] = __builtin_amdgcn_readlane(st.w[i], src);
         before -= w[i];
       }
       x -= base + before;
@@ -368,10 +382,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
         }
       u.load(a, b);
       u.k = 0;
-      if (u.n == 1) {
+      if (kOne) {
         const uint32_t s = u.steps(a);
-        u.k = (uint32_t)quot(x, s);
-        x -= (uint64_t)u.k * s;
+        u.k = min(x / s, u.tiles - 1);
+        x -= u.k * s;
       } else {
         for (uint32_t s = u.steps(a); x >= s && u.k + 1 < u.tiles; s = u.steps(a)) {
           x -= s;
@@ -382,16 +396,15 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
     }
     off = x;
   }
-  const uint64_t piece = at;
-  if (threadIdx.x == 0 && a.info) static_cast<JoinInfo *>(a.info)[blockIdx.x].valid = 0;
+  const uint32_t piece = at;
   const Scale sc_q = scale_of(a.scale);
   const TC *kcache = static_cast<const TC *>(a.k), *vcache = static_cast<const TC *>(a.v);
   bool bad = false;
 
-  while (at < stop) {
+  while (at < stop && hk < a.n_kv_heads) {
     // the part of row tile u.k that this workgroup holds: steps [s_lo, s_hi)
     const uint32_t steps = u.steps(a);
-    const uint32_t left = (uint32_t)min((uint64_t)(steps - (uint32_t)off), stop - at);
+    const uint32_t left = min(steps - off, stop - at);
     const Tile t{u.b, u.row0, u.n, u.k * kRowTile, min(kRowTile, u.n * a.group - u.k * kRowTile)};
     const bool live = n16 < t.rows;
     const Row row = row_of(a, t, u.len, t.first + (live ? n16 : 0));
@@ -399,19 +412,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
     const Row r_last = row_of(a, t, u.len, t.first + t.rows - 1);
     const int32_t begin = r_first.lo, end = r_last.hi;  // lo and hi grow with the row
     const int32_t tiles = end > begin ? (int32_t)(((uint32_t)(end - begin) + kTok - 1) / kTok) : 0;
-    const int32_t t_lo = a.whole ? 0 : (int32_t)off;
-    const int32_t t_hi = a.whole ? tiles : min(tiles, (int32_t)((uint32_t)off + left));
+    // a step is 2^(step_shift - 5) tiles
+    const uint32_t per_step = a.step_shift - 5;
+    const int32_t t_lo = a.whole ? 0 : (int32_t)(off << per_step);
+    const int32_t t_hi = a.whole ? tiles : min(tiles, (int32_t)((off + left) << per_step));
     const uint32_t qh = hk * a.group + row.head;
-
-    u32x4 qf[KK];
-#pragma unroll
-    for (int kk = 0; kk < KK; ++kk) qf[kk] = u32x4{0, 0, 0, 0};
-    if (live) {
-      const TI *q = static_cast<const TI *>(a.q) + (uint64_t)row.token * a.q_stride +
-                    (uint64_t)qh * D + g4 * 8;
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk) qf[kk] = load_q8<TI, TC>(q + kk * 32, sc_q);
-    }
 
     float m = ninf(), l = 0.0f;
     f32x4 o[E];
@@ -422,22 +427,35 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
     const int32_t last = end - 1;
     // Each lane looks up one token of a tile (the others' slots come by
     // shuffle), a tile ahead of its use.
-    uint32_t ahead = 0;
+    uint32_t next_id = 0, next_in = 0;  // page id; token within the page
     auto look_up = [&](int32_t ti) {
       int32_t j = begin + ti * (int32_t)kTok + (int32_t)(lane & 31);
       j = j < last ? j : last;
-      bad = !slot_of(table, a.s.page, a.s.n_pages, (uint32_t)j, ahead) || bad;
+      const uint32_t page = a.s.page.div((uint32_t)j);
+      next_id = (uint32_t)table[page];
+      next_in = (uint32_t)j - page * a.s.page.d;
     };
     if (t_lo + (int32_t)wave < t_hi) look_up(t_lo + (int32_t)wave);
+    u32x4 qf[KK];
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) qf[kk] = u32x4{0, 0, 0, 0};
+    if (live) {
+      const TI *q = static_cast<const TI *>(a.q) + (uint64_t)row.token * a.q_stride +
+                    (uint64_t)qh * D + g4 * 8;
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) qf[kk] = load_q8<TI, TC>(q + kk * 32, sc_q);
+    }
+
 
     for (int32_t ti = t_lo + (int32_t)wave; ti < t_hi; ti += 4) {
       const int32_t j0 = begin + ti * (int32_t)kTok;
       // slots of this lane's two key rows and eight value rows
-      uint32_t kslot[2], vslot[8];
-      kslot[0] = __shfl(ahead, n16);
-      kslot[1] = __shfl(ahead, 16 + n16);
+      uint32_t slot, kslot[2], vslot[8];
+      bad = !a.s.slot_in(next_id, next_in, slot) || bad;
+      kslot[0] = __shfl(slot, n16);
+      kslot[1] = __shfl(slot, 16 + n16);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) vslot[i] = __shfl(ahead, (i >> 2) * 16 + g4 * 4 + (i & 3));
+      for (int i = 0; i < 8; ++i) vslot[i] = __shfl(slot, (i >> 2) * 16 + g4 * 4 + (i & 3));
       u32x4 kf[2][KK];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -614,14 +632,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
         }
       }
     }
-    if (threadIdx.x == 0 && off == 0 && left < steps) {
-      JoinInfo *info = static_cast<JoinInfo *>(a.info) + blockIdx.x;
-      info->b = u.b;
-      info->k = u.k;
-      info->head = hk;
-      info->last = pc.owner(at + steps - 1);
-      info->slot = slot;
-      info->valid = 1;
+    if (threadIdx.x == 0 && off == 0 && info) {
+      const bool cut = left < steps;
+      const bool by_unit = kOne && a.by_unit;
+      const uint32_t id = by_unit ? (u.b * per + u.k) * a.n_kv_heads + hk : blockIdx.x;
+      if (cut)
+        info[id] = JoinInfo{1, u.b, u.k, hk, blockIdx.x, pc.owner(at + steps - 1), slot, 0};
+      else if (by_unit)
+        info[id].cut = 0;
     }
     at += left;
     off = 0;
@@ -633,85 +651,81 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
   if (__ballot(bad) && lane == 0) set_status(a.status, KVC_ERR_SHAPE);
 }
 
-// Joins the parts of a row tile that k_attend_rows cut: one workgroup for
-// each of its workgroups, which has work if that one held a row tile's first
-// part and not its last.  16 waves share the rows; the waves of a row share
-// the parts and are added up through LDS in a fixed order.
+// Joins the parts of a row tile that k_attend_rows cut: a workgroup for each
+// JoinInfo and row.  Four waves share the parts and are added up through LDS
+// in a fixed order.
 template <class TI, class TC, int D>
-__global__ __launch_bounds__(1024) void k_attend_rows_join(AttendArgs a) {
+__global__ __launch_bounds__(256) void k_attend_rows_join(AttendArgs a) {
   constexpr int N = D > 128 ? 4 : D > 64 ? 2 : 1;  // dimensions a lane
-  __shared__ float s_acc[16][D];
+  __shared__ float s_acc[4][D];
   const JoinInfo info = static_cast<const JoinInfo *>(a.info)[blockIdx.x];
-  if (!info.valid) return;
-  const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  if (info.cut != 1 || info.b >= a.s.n_seqs || info.last >= a.pieces) return;
+  const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = blockIdx.y;
   uint32_t row0, n;
   a.s.rows(info.b, row0, n);
+  if (info.k * kRowTile >= n * a.group) return;
   const Tile t{info.b, row0, n, info.k * kRowTile, min(kRowTile, n * a.group - info.k * kRowTile)};
-  uint32_t per = 16;  // waves to a row
-  while (per > 1 && per * t.rows > 16) per >>= 1;
-  const uint32_t r = wave / per, sub = wave - r * per;
-  const bool live = r < t.rows;
-  const uint32_t parts = info.last - blockIdx.x + 1;
+  if (r >= t.rows) return;
+  const uint32_t parts = info.last - info.first + 1;
   auto part_of = [&](uint32_t i) {
-    return i == 0 ? (uint64_t)blockIdx.x * 2 + info.slot : (uint64_t)(blockIdx.x + i) * 2;
+    return (uint64_t)(info.first + i) * 2 + (i == 0 ? info.slot : 0);
   };
   float mm = ninf(), l = 0.0f, acc[N] = {};
-  float ref = 0.0f;
   const bool mine = lane * N < D;
-  if (live) {
-    for (uint32_t i = lane; i < parts; i += 64)
-      mm = __builtin_fmaxf(mm, a.part_ml[part_of(i) * 32 + r]);
+  for (uint32_t i = lane; i < parts; i += 64)
+    mm = __builtin_fmaxf(mm, a.part_ml[part_of(i) * 32 + r]);
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) mm = __builtin_fmaxf(mm, __shfl_xor(mm, d));
-    ref = mm == ninf() ? 0.0f : mm;
-    for (uint32_t i0 = 0; i0 < parts; i0 += 64) {
-      float f = 0.0f;
-      if (i0 + lane < parts) {
-        const uint64_t p = part_of(i0 + lane);
-        f = __builtin_amdgcn_exp2f(a.part_ml[p * 32 + r] - ref);
-        l = __builtin_fmaf(a.part_ml[p * 32 + 16 + r], f, l);
-      }
-      const uint32_t here = min(64u, parts - i0);
-      // eight parts' loads in flight; past the last one: the last one times 0
-      for (uint32_t i = sub; i < here; i += 8 * per) {
-        float fi[8], x[8][N];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t ij = i + j * per, ic = min(ij, here - 1);
-          fi[j] = ij < here ? __shfl(f, (int)ic) : 0.0f;
-          const float *op = a.part + (part_of(i0 + ic) * 16 + r) * D + lane * N;
-#pragma unroll
-          for (int e = 0; e < N; ++e) x[j][e] = mine ? op[e] : 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int e = 0; e < N; ++e)
-            acc[e] = fi[j] == 0.0f ? acc[e] : __builtin_fmaf(x[j][e], fi[j], acc[e]);
-      }
+  for (int d = 1; d < 64; d <<= 1) mm = __builtin_fmaxf(mm, __shfl_xor(mm, d));
+  const float ref = mm == ninf() ? 0.0f : mm;
+  for (uint32_t i0 = 0; i0 < parts; i0 += 64) {
+    float f = 0.0f;
+    if (i0 + lane < parts) {
+      const uint64_t p = part_of(i0 + lane);
+      f = __builtin_amdgcn_exp2f(a.part_ml[p * 32 + r] - ref);
+      l = __builtin_fmaf(a.part_ml[p * 32 + 16 + r], f, l);
     }
+    const uint32_t here = min(64u, parts - i0);
+    // eight parts' loads in flight; past the last one: the last one, unused
+    for (uint32_t i = wave; i < here; i += 32) {
+      float fi[8], x[8][N];
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
-    if (mine)
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t ij = i + j * 4, ic = min(ij, here - 1);
+        const float fc = __shfl(f, (int)ic);
+        fi[j] = ij < here ? fc : 0.0f;
+        const float *op = a.part + (part_of(i0 + ic) * 16 + r) * D + lane * N;
 #pragma unroll
-      for (int e = 0; e < N; ++e) s_acc[wave][lane * N + e] = acc[e];
+        for (int e = 0; e < N; ++e) x[j][e] = mine ? op[e] : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          acc[e] = fi[j] == 0.0f ? acc[e] : __builtin_fmaf(x[j][e], fi[j], acc[e]);
+    }
   }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
+  if (mine)
+#pragma unroll
+    for (int e = 0; e < N; ++e) s_acc[wave][lane * N + e] = acc[e];
   __syncthreads();
-  if (!live || sub != 0) return;
   const Row row = row_of(a, t, a.s.len(info.b), t.first + r);
   const bool some = row.hi > row.lo;
   const float inv = some ? 1.0f / l : 0.0f;
   const uint32_t h = info.head * a.group + row.head;
   TI *out = static_cast<TI *>(a.out) + (uint64_t)row.token * a.out_stride + (uint64_t)h * D;
-  for (uint32_t x = lane * 2; x < D; x += 128) {
+  if (threadIdx.x < D / 2) {
+    const uint32_t x = threadIdx.x * 2;
     float v0 = 0.0f, v1 = 0.0f;
-    for (uint32_t w = 0; w < per; ++w) {
-      v0 += s_acc[wave + w][x];
-      v1 += s_acc[wave + w][x + 1];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      v0 += s_acc[w][x];
+      v1 += s_acc[w][x + 1];
     }
     *reinterpret_cast<uint32_t *>(out + x) = some ? pack2<TI>(v0 * inv, v1 * inv) : 0u;
   }
-  if (lane == 0 && a.lse)
+  if (threadIdx.x == 0 && a.lse)
     a.lse[(uint64_t)row.token * a.n_heads + h] =
         some ? (mm - kShift<TC> + __builtin_amdgcn_logf(l)) * kLn2 : ninf();
 }
@@ -845,7 +859,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_tile(AttendArg
     for (int i = 0; i < NC; ++i) {
       int32_t j = j0 + (int32_t)((threadIdx.x + 256 * i) / CH);
       j = j < last ? j : last;
-      bad = !slot_of(table, a.s.page, a.s.n_pages, (uint32_t)j, slot[i]) || bad;
+      bad = !a.s.slot_of(table, (uint32_t)j, slot[i]) || bad;
     }
   };
   auto load_tile = [&]() {
@@ -967,7 +981,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_tile(AttendArg
         pj = __shfl(pj, (int)(n32 + 32 * ((e >> 2) & 1)));
         const int32_t j = j0 + (int32_t)jt;
         uint32_t sj;
-        slot_of(table, a.s.page, a.s.n_pages, (uint32_t)(j < last ? j : last), sj);
+        a.s.slot_of(table, (uint32_t)(j < last ? j : last), sj);
         if (j >= row.lo && j < row.hi) {
           const TC *vp = vbase + (uint64_t)sj * a.row + hi * 4;
 #pragma unroll
@@ -1091,6 +1105,9 @@ struct Plan {
   uint32_t rows;      // 16 or 128 to a workgroup
   uint32_t grid;      // workgroups of the 16-row kernel
   bool whole, join;   // it cuts no row tile; a second launch is needed
+  bool by_unit;       // JoinInfo records: one for each row tile and KV head
+  uint64_t infos;
+  uint32_t shift;     // log2 of the tokens of a step
   uint32_t tiles, splits;             // of the 128-row kernel
   uint64_t part, part_ml, info, total;  // workspace offsets
 };
@@ -1118,14 +1135,21 @@ Plan make_plan(const kvc_paged_desc &p, const kvc_paged_batch &b) {
   const uint64_t units = (uint64_t)w.tiles * p.n_kv_heads;
   uint64_t parts = 0;
   if (w.rows == 16) {
-    const uint64_t steps = std::max<uint64_t>(1, ((uint64_t)b.max_len + kTok - 1) / kTok);
+    uint64_t steps = std::max<uint64_t>(1, ((uint64_t)b.max_len + kTok - 1) / kTok);
     w.whole = steps <= kWholeSteps;
+    w.shift = 5;
+    while (!w.whole && units * steps >= (1ull << 31)) {
+      ++w.shift;
+      steps = (steps + 1) / 2;
+    }
     if (w.whole) {
       // each row tile once; a batch of single tokens needs no search for it
       w.grid = (uint32_t)(b.q_start ? std::min<uint64_t>(units, 4 * slots) : units);
     } else {
       w.grid = (uint32_t)std::min<uint64_t>(slots, (units * steps + kMinSteps - 1) / kMinSteps);
       w.join = true;
+      w.by_unit = !b.q_start && units < w.grid;
+      w.infos = w.by_unit ? units : w.grid;
       parts = 2ull * w.grid;
     }
   } else {
@@ -1139,7 +1163,7 @@ Plan make_plan(const kvc_paged_desc &p, const kvc_paged_batch &b) {
   if (w.join) {
     w.part_ml = parts * w.rows * p.head_dim * 4;
     w.info = w.part_ml + parts * w.rows * 2 * 4;
-    w.total = w.info + (w.rows == 16 ? (uint64_t)w.grid * sizeof(JoinInfo) : 0);
+    w.total = w.info + w.infos * sizeof(JoinInfo);
     w.total = (w.total + 255) & ~uint64_t(255);
   }
   return w;
@@ -1149,9 +1173,15 @@ template <class TI, class TC, int D>
 hipError_t launch_d(const AttendArgs &a, const Plan &w, hipStream_t stream) {
   const uint32_t units = w.tiles * a.n_kv_heads;
   if (w.rows == 16) {
-    hipLaunchKernelGGL((k_attend_rows<TI, TC, D>), dim3(w.grid), dim3(256), 0, stream, a);
+    if (a.s.q_start)
+      hipLaunchKernelGGL((k_attend_rows<TI, TC, D, false>), dim3(w.grid), dim3(256), 0, stream, a);
+    else
+      hipLaunchKernelGGL((k_attend_rows<TI, TC, D, true>), dim3(w.grid), dim3(256), 0, stream, a);
     if (w.join)
-      hipLaunchKernelGGL((k_attend_rows_join<TI, TC, D>), dim3(w.grid), dim3(1024), 0, stream, a);
+      hipLaunchKernelGGL((k_attend_rows_join<TI, TC, D>),
+                         dim3((uint32_t)w.infos, a.s.q_start ? kRowTile
+                                                             : std::min(kRowTile, a.group)),
+                         dim3(256), 0, stream, a);
   } else {
     hipLaunchKernelGGL((k_attend_tile<TI, TC, D>), dim3(units * w.splits), dim3(256), kBigLds<D>,
                        stream, a);
@@ -1184,6 +1214,9 @@ hipError_t launch_attend(const kvc_paged_desc &p, const kvc_paged_batch &b, Atte
   const Plan w = make_plan(p, b);
   a.splits = w.splits;
   a.whole = w.whole;
+  a.step_shift = w.shift;
+  a.by_unit = w.by_unit;
+  a.pieces = w.grid;
   a.min_steps = kMinSteps;
   uint8_t *base = static_cast<uint8_t *>(ws);
   a.part = reinterpret_cast<float *>(base + w.part);

@@ -85,27 +85,28 @@ struct Seqs {
            (q_start[b] < 0 || q_start[b + 1] < q_start[b] || q_start[b + 1] > (int32_t)n_tokens);
   }
   // the length, within [0, max_len]
-  __host__ __device__ inline int32_t len(uint32_t b) const {
-    const int32_t m = lens[b];
+  __host__ __device__ inline int32_t clamp_len(int32_t m) const {
     return m < 0 ? 0 : m > (int32_t)max_len ? (int32_t)max_len : m;
   }
-  __host__ __device__ inline bool len_bad(uint32_t b) const {
-    return lens[b] < 0 || lens[b] > (int32_t)max_len;
+  __host__ __device__ inline bool len_out(int32_t m) const {
+    return m < 0 || m > (int32_t)max_len;
+  }
+  __host__ __device__ inline int32_t len(uint32_t b) const { return clamp_len(lens[b]); }
+  __host__ __device__ inline bool len_bad(uint32_t b) const { return len_out(lens[b]); }
+  // Slot (token row of the pool) of token `in` of page `id`.  False for an id
+  // outside the pool; the slot is then one inside it, so that a caller that
+  // goes on reads nothing out of bounds.
+  __host__ __device__ inline bool slot_in(uint32_t id, uint32_t in, uint32_t &slot) const {
+    const bool ok = id < n_pages;
+    slot = (ok ? id : 0) * page.d + in;
+    return ok;
+  }
+  // ... of token j, 0 <= j < max_len, of the sequence with page ids `ids`
+  __host__ __device__ inline bool slot_of(const int32_t *ids, uint32_t j, uint32_t &slot) const {
+    const uint32_t e = page.div(j);
+    return slot_in((uint32_t)ids[e], j - e * page.d, slot);
   }
 };
-
-// Slot (token row of the pool) of token j, 0 <= j < max_len, of the sequence
-// with page ids `table`.  False for an id outside the pool; the slot is then
-// one inside it, so that a caller that goes on reads nothing out of bounds.
-__host__ __device__ inline bool slot_of(const int32_t *table, const FastDiv &page,
-                                        uint32_t n_pages, uint32_t j, uint32_t &slot) {
-  const uint32_t e = page.div(j);
-  uint32_t id = (uint32_t)table[e];
-  const bool ok = id < n_pages;
-  if (!ok) id = 0;
-  slot = id * page.d + (j - e * page.d);
-  return ok;
-}
 
 hipError_t launch_append(const kvc_paged_desc &p, const Seqs &s, uint32_t layer, void *pool,
                          const void *k, uint64_t k_stride, const void *v, uint64_t v_stride,
@@ -132,7 +133,10 @@ struct AttendArgs {
   uint32_t n_heads, n_kv_heads, group;
   FastDiv group_div;
   uint32_t splits;     // of the 128-row kernel
-  uint32_t min_steps;  // of the 16-row kernel: tiles a workgroup takes at least
+  uint32_t step_shift;  // log2 of the tokens of a step of the 16-row kernel, at least 5
+  uint32_t min_steps;  // of the 16-row kernel: steps a workgroup takes at least
+  uint32_t pieces;     // its workgroups
+  bool by_unit;        // the layout of its join records
   bool whole;          // the 16-row kernel cuts no row tile
   float scale;      // scale * log2(e)
   uint32_t window;

@@ -164,8 +164,7 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
   const int32_t pos = a.s.lens[b] - (int32_t)n + (int32_t)(row - r0);
   if (pos < 0) return;  // padding
   uint32_t slot;
-  if (!slot_of(a.s.table + (uint64_t)b * a.s.table_stride, a.s.page, a.s.n_pages, (uint32_t)pos,
-               slot) ||
+  if (!a.s.slot_of(a.s.table + (uint64_t)b * a.s.table_stride, (uint32_t)pos, slot) ||
       (a.rotary && (uint32_t)pos >= a.n_positions)) {
     if (first) set_status(a.status, KVC_ERR_SHAPE);
     return;
@@ -191,11 +190,11 @@ constexpr uint32_t kPageRows = 16;
 
 struct PageArgs {
   uint8_t *pool, *flat;
-  const int32_t *table;
+  Seqs s;                          // its pages and page table
   uint64_t row;                    // bytes of a token's row
   uint64_t pool_tokens, T_total;   // token rows of a (layer, K/V) plane
-  uint32_t first, n, flat_first, n_pages;
-  FastDiv page, vecs;              // vecs: 16-byte vectors of a row
+  uint32_t first, n, flat_first;
+  FastDiv vecs;                    // 16-byte vectors of a row
   int32_t *status;
 };
 
@@ -207,7 +206,7 @@ __global__ __launch_bounds__(256) void k_page_copy(PageArgs a) {
   if (threadIdx.x < rows) {
     uint32_t at;
     int64_t slot = -1;
-    if (slot_of(a.table, a.page, a.n_pages, a.first + t0 + threadIdx.x, at))
+    if (a.s.slot_of(a.s.table, a.first + t0 + threadIdx.x, at))
       slot = at;
     else if (blockIdx.y == 0)
       set_status(a.status, KVC_ERR_SHAPE);
@@ -402,15 +401,15 @@ hipError_t launch_page_copy(const kvc_paged_desc &p, void *pool, const int32_t *
   PageArgs a{};
   a.pool = static_cast<uint8_t *>(pool);
   a.flat = static_cast<uint8_t *>(flat);
-  a.table = table;
+  a.s.table = table;
   a.row = (uint64_t)p.n_kv_heads * p.head_dim * 2;
   a.pool_tokens = (uint64_t)p.n_pages * p.page_tokens;
   a.T_total = T_total;
   a.first = first_token;
   a.n = n_tokens;
   a.flat_first = flat_first;
-  a.n_pages = p.n_pages;
-  a.page = FastDiv::make(p.page_tokens);
+  a.s.n_pages = p.n_pages;
+  a.s.page = FastDiv::make(p.page_tokens);
   a.vecs = FastDiv::make(p.n_kv_heads * p.head_dim / 8);
   a.status = status;
   const dim3 grid((n_tokens + kPageRows - 1) / kPageRows, 2 * p.n_layers);

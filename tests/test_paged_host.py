@@ -211,11 +211,13 @@ int main() {
   }
   // slots: ids outside the pool give false and a slot inside it
   const int32_t table[] = {4, -1, 0, 5, 1000000, (int32_t)0x80000000, 3};
-  const FastDiv page = FastDiv::make(20);
+  Seqs pool{};
+  pool.page = FastDiv::make(20);
+  pool.n_pages = 5;
   for (uint32_t j = 0; j < 140; ++j) {
     uint32_t slot = 0xFFFFFFFFu;
     const int32_t id = table[j / 20];
-    const bool ok = slot_of(table, page, 5, j, slot);
+    const bool ok = pool.slot_of(table, j, slot);
     CHECK(ok == (id >= 0 && id < 5));
     CHECK(slot < 100);
     if (ok) CHECK(slot == (uint32_t)id * 20 + j % 20);
