@@ -93,30 +93,32 @@ __device__ inline u32x4 load_q8(const TI *p, const Scale &sc) {
   return w;
 }
 
-// N dwords from a 4-byte aligned address (more where N allows it).
 template <int N>
 struct Words {
   uint32_t w[N];
 };
+// N dwords from a 4-byte aligned address, used once: marked so that they do
+// not stay in the caches (an eighth faster than plain loads where HBM is the bound; the
+// keys' loads, which take half a cache line at a time, are better kept).
 template <int N>
-__device__ inline Words<N> load_words(const void *p) {
+__device__ inline Words<N> stream_words(const void *p) {
   Words<N> r;
   if constexpr (N % 4 == 0) {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
-      const u32x4 v = load16(static_cast<const uint32_t *>(p) + 4 * i);
+      const u32x4 v = __builtin_nontemporal_load(static_cast<const u32x4 *>(p) + i);
 #pragma unroll
       for (int e = 0; e < 4; ++e) r.w[4 * i + e] = v[e];
     }
   } else if constexpr (N == 3) {
     typedef uint32_t u32x3 __attribute__((ext_vector_type(3), aligned(4)));
-    const u32x3 v = *static_cast<const u32x3 *>(p);
+    const u32x3 v = __builtin_nontemporal_load(static_cast<const u32x3 *>(p));
     r.w[0] = v[0];
     r.w[1] = v[1];
     r.w[2] = v[2];
   } else {
     static_assert(N == 2, "head dimension");
-    const u32x2 v = *static_cast<const u32x2 *>(p);
+    const u32x2 v = __builtin_nontemporal_load(static_cast<const u32x2 *>(p));
     r.w[0] = v[0];
     r.w[1] = v[1];
   }
@@ -170,9 +172,13 @@ __device__ inline Row row_of(const AttendArgs &a, const Tile &t, int32_t len, ui
 // lengths are.  A workgroup that holds all of a row tile's steps writes its
 // rows' outputs; one that holds a part writes its sums, maxima and
 // unnormalised output to the workspace (at most two parts, at its piece's two
-// ends) and k_attend_join adds them up.  All heads have the same row tiles,
-// so the workgroups of different heads run over the same tokens at the same
-// time, and their short rows (head_dim elements) make up whole cached tokens.
+// ends) and k_attend_rows_join adds them up.
+//
+// A workgroup's four waves take four neighbouring KV heads of the same tokens
+// where there are so many (two and two, or one, otherwise: then the waves of
+// a head take its tiles in turn and are joined through LDS): a head's rows
+// are short, and four side by side are fetched from HBM a tenth faster than
+// four rows of one head.  "Head" below is such a group of a.wg_heads heads.
 //
 // Where no cache is longer than a few steps (`whole`), every row tile counts
 // as one step, is never cut, and needs no join.
@@ -323,14 +329,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
 
   // this workgroup's piece of the line, and where it begins
   Work<kOne> u;
-  uint32_t hk;
+  uint32_t hg;
   uint32_t at, stop, off;  // off: steps of the first row tile before the piece
   Pieces pc{gridDim.x, 1, 0};
   JoinInfo *info = static_cast<JoinInfo *>(a.info);
   const uint32_t per = Work<kOne>::tiles_of(a, 1);  // row tiles of a single token
   if (kOne && a.whole) {  // a row tile to a workgroup: no search
-    const uint32_t unit = blockIdx.x / a.n_kv_heads;
-    hk = blockIdx.x - unit * a.n_kv_heads;
+    const uint32_t unit = blockIdx.x / a.head_groups;
+    hg = blockIdx.x - unit * a.head_groups;
     u.load(a, unit / per);
     u.k = unit - u.b * per;
     at = off = 0;
@@ -346,7 +352,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
       st.load(a, b0, check);
       total += __builtin_amdgcn_readlane(st.upto, 63);
     }
-    const uint32_t line = total * a.n_kv_heads;
+    const uint32_t line = total * a.head_groups;
     // at least min_steps to a workgroup
     pc.parts = min(gridDim.x, a.whole ? line : (line + a.min_steps - 1) / a.min_steps);
     if (blockIdx.x >= pc.parts) return;
@@ -354,8 +360,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
     pc.rem = line - pc.per * pc.parts;
     at = pc.start(blockIdx.x);
     stop = pc.start(blockIdx.x + 1);
-    hk = at / total;
-    uint32_t x = at - hk * total;
+    hg = at / total;
+    uint32_t x = at - hg * total;
     uint32_t base = 0;
     for (uint32_t b0 = 0;; b0 += 256) {  // some sequence holds step x < total
       if (b0 >= a.s.n_seqs) return;
@@ -401,7 +407,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
   const TC *kcache = static_cast<const TC *>(a.k), *vcache = static_cast<const TC *>(a.v);
   bool bad = false;
 
-  while (at < stop && hk < a.n_kv_heads) {
+  const uint32_t turns = 4 / a.wg_heads;  // waves to a head
+  const uint32_t my_head = wave / turns, turn = wave - my_head * turns;
+  while (at < stop && hg < a.head_groups) {
+    const uint32_t hk = hg * a.wg_heads + my_head;
     // the part of row tile u.k that this workgroup holds: steps [s_lo, s_hi)
     const uint32_t steps = u.steps(a);
     const uint32_t left = min(steps - off, stop - at);
@@ -435,7 +444,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
       next_id = (uint32_t)table[page];
       next_in = (uint32_t)j - page * a.s.page.d;
     };
-    if (t_lo + (int32_t)wave < t_hi) look_up(t_lo + (int32_t)wave);
+    if (t_lo + (int32_t)turn < t_hi) look_up(t_lo + (int32_t)turn);
     u32x4 qf[KK];
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) qf[kk] = u32x4{0, 0, 0, 0};
@@ -447,7 +456,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
     }
 
 
-    for (int32_t ti = t_lo + (int32_t)wave; ti < t_hi; ti += 4) {
+    for (int32_t ti = t_lo + (int32_t)turn; ti < t_hi; ti += (int32_t)turns) {
       const int32_t j0 = begin + ti * (int32_t)kTok;
       // slots of this lane's two key rows and eight value rows
       uint32_t slot, kslot[2], vslot[8];
@@ -466,9 +475,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
       Words<E / 2> vf[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        vf[i] = load_words<E / 2>(vbase + (uint64_t)vslot[i] * a.row + n16 * E);
+        vf[i] = stream_words<E / 2>(vbase + (uint64_t)vslot[i] * a.row + n16 * E);
 
-      if (ti + 4 < t_hi) look_up(ti + 4);
+      if (ti + (int32_t)turns < t_hi) look_up(ti + (int32_t)turns);
 
       f32x4 sc[2];
 #pragma unroll
@@ -573,25 +582,28 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
 
-    // join the waves: each one's sums times exp2(its maximum - the common one)
-    if (lane < 16) {
-      s_m[wave][lane] = m;
-      s_l[wave][lane] = l;
-    }
-    __syncthreads();
-    float mm = ninf(), ll = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) mm = __builtin_fmaxf(mm, s_m[w][n16]);
-    const float mref = mm == ninf() ? 0.0f : mm;
-#pragma unroll
-    for (int w = 0; w < 4; ++w)
-      ll = __builtin_fmaf(s_l[w][n16], __builtin_amdgcn_exp2f(s_m[w][n16] - mref), ll);
     const bool some = row.hi > row.lo;
     const bool single = off == 0 && left == steps;
-    const float f = __builtin_amdgcn_exp2f(m - mref) * (single ? (some ? 1.0f / ll : 0.0f) : 1.0f);
     const uint32_t slot = at == piece ? 0 : 1;
-    const uint64_t part = (uint64_t)blockIdx.x * 2 + slot;
-    if (wave == 0 && lane < t.rows) {
+    const uint64_t part = ((uint64_t)blockIdx.x * 2 + slot) * a.wg_heads + my_head;
+    float mm = m, ll = l;
+    if (turns > 1) {  // the common maximum of the head's waves and their sum
+      if (lane < 16) {
+        s_m[wave][lane] = m;
+        s_l[wave][lane] = l;
+      }
+      __syncthreads();
+      for (uint32_t w = 0; w < turns; ++w)
+        mm = __builtin_fmaxf(mm, s_m[my_head * turns + w][n16]);
+      ll = 0.0f;
+      for (uint32_t w = 0; w < turns; ++w)
+        ll = __builtin_fmaf(s_l[my_head * turns + w][n16],
+                            __builtin_amdgcn_exp2f(s_m[my_head * turns + w][n16] -
+                                                   (mm == ninf() ? 0.0f : mm)), ll);
+    }
+    const float f = __builtin_amdgcn_exp2f(m - (mm == ninf() ? 0.0f : mm)) *
+                    (single ? (some ? 1.0f / ll : 0.0f) : 1.0f);
+    if (turn == 0 && lane < t.rows) {
       if (!single) {
         a.part_ml[part * 32 + lane] = mm;
         a.part_ml[part * 32 + 16 + lane] = ll;
@@ -600,59 +612,87 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
             some ? (mm - kShift<TC> + __builtin_amdgcn_logf(ll)) * kLn2 : ninf();
       }
     }
-#pragma unroll
-    for (int e0 = 0; e0 < E; e0 += EC) {
-      if (e0) __syncthreads();
-#pragma unroll
-      for (int e = 0; e < EC; ++e)
+    TI *out = static_cast<TI *>(a.out) + (uint64_t)row.token * a.out_stride + (uint64_t)qh * D;
+    float *part_o = a.part + (part * 16 + n16) * D;
+    if (turns == 1) {
+      // a lane's 4E values are dimensions g4 * 4E on of its row
+      if (live) {
+        float v[4 * E];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          s_o[wave][n16][(g4 * 4 + c) * EC + e] = o[e0 + e][c] * f;
-      __syncthreads();
-      // 16 rows of 16 * EC dimensions, two at a time; dimension k * E + e0 + e
-      for (uint32_t i = threadIdx.x; i < t.rows * 8u * EC; i += 256) {
-        const uint32_t r = i / (8u * EC), x = (i - r * (8u * EC)) * 2;
-        float v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          v0 += s_o[w][r][x];
-          v1 += s_o[w][r][x + 1];
-        }
-        const uint32_t dim = E == EC ? x : (x / EC) * E + e0 + x % EC;
+          for (int e = 0; e < E; ++e) v[c * E + e] = o[e][c] * f;
         if (single) {
-          const Row w = row_of(a, t, u.len, t.first + r);
-          uint32_t *op = reinterpret_cast<uint32_t *>(
-              static_cast<TI *>(a.out) + (uint64_t)w.token * a.out_stride +
-              (uint64_t)(hk * a.group + w.head) * D + dim);
-          *op = w.hi > w.lo ? pack2<TI>(v0, v1) : 0u;
+#pragma unroll
+          for (int i = 0; i < E / 2; ++i) {
+            u32x4 w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = some ? pack2<TI>(v[8 * i + 2 * e], v[8 * i + 2 * e + 1]) : 0u;
+            store16(out + g4 * 4 * E + 8 * i, w);
+          }
         } else {
-          float *op = a.part + (part * 16 + r) * D + dim;
-          op[0] = v0;
-          op[1] = v1;
+#pragma unroll
+          for (int i = 0; i < E; ++i)
+            *reinterpret_cast<f32x4 *>(part_o + g4 * 4 * E + 4 * i) =
+                f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e0 = 0; e0 < E; e0 += EC) {
+        if (e0) __syncthreads();
+#pragma unroll
+        for (int e = 0; e < EC; ++e)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            s_o[wave][n16][(g4 * 4 + c) * EC + e] = o[e0 + e][c] * f;
+        __syncthreads();
+        // the head's waves add up 16 rows of 16 * EC dimensions, two dimensions
+        // at a time; x of them stands for dimension x / EC * E + e0 + x % EC
+        for (uint32_t i = turn * 64 + lane; i < t.rows * 8u * EC; i += turns * 64) {
+          const uint32_t r = i / (8u * EC), x = (i - r * (8u * EC)) * 2;
+          float v0 = 0.0f, v1 = 0.0f;
+          for (uint32_t w = 0; w < turns; ++w) {
+            v0 += s_o[my_head * turns + w][r][x];
+            v1 += s_o[my_head * turns + w][r][x + 1];
+          }
+          const uint32_t dim = E == EC ? x : (x / EC) * E + e0 + x % EC;
+          if (single) {
+            const Row w = row_of(a, t, u.len, t.first + r);
+            uint32_t *op = reinterpret_cast<uint32_t *>(
+                static_cast<TI *>(a.out) + (uint64_t)w.token * a.out_stride +
+                (uint64_t)(hk * a.group + w.head) * D + dim);
+            *op = w.hi > w.lo ? pack2<TI>(v0, v1) : 0u;
+          } else {
+            float *op = a.part + (part * 16 + r) * D + dim;
+            op[0] = v0;
+            op[1] = v1;
+          }
         }
       }
     }
     if (threadIdx.x == 0 && off == 0 && info) {
       const bool cut = left < steps;
       const bool by_unit = kOne && a.by_unit;
-      const uint32_t id = by_unit ? (u.b * per + u.k) * a.n_kv_heads + hk : blockIdx.x;
+      const uint32_t id = by_unit ? (u.b * per + u.k) * a.head_groups + hg : blockIdx.x;
       if (cut)
-        info[id] = JoinInfo{1, u.b, u.k, hk, blockIdx.x, pc.owner(at + steps - 1), slot, 0};
+        info[id] = JoinInfo{1, u.b, u.k, hg, blockIdx.x, pc.owner(at + steps - 1), slot, 0};
       else if (by_unit)
         info[id].cut = 0;
     }
     at += left;
     off = 0;
     if (at < stop) {
-      u.next(a, hk);
-      __syncthreads();  // s_m, s_l and s_o are free again
+      u.next(a, hg);
+      if (turns > 1) __syncthreads();  // s_m, s_l and s_o are free again
     }
   }
   if (__ballot(bad) && lane == 0) set_status(a.status, KVC_ERR_SHAPE);
 }
 
 // Joins the parts of a row tile that k_attend_rows cut: a workgroup for each
-// JoinInfo and row.  Four waves share the parts and are added up through LDS
+// JoinInfo, row and head of the group.  Four waves share the parts and are added up through LDS
 // in a fixed order.
 template <class TI, class TC, int D>
 __global__ __launch_bounds__(256) void k_attend_rows_join(AttendArgs a) {
@@ -668,7 +708,7 @@ __global__ __launch_bounds__(256) void k_attend_rows_join(AttendArgs a) {
   if (r >= t.rows) return;
   const uint32_t parts = info.last - info.first + 1;
   auto part_of = [&](uint32_t i) {
-    return (uint64_t)(info.first + i) * 2 + (i == 0 ? info.slot : 0);
+    return ((uint64_t)(info.first + i) * 2 + (i == 0 ? info.slot : 0)) * a.wg_heads + blockIdx.z;
   };
   float mm = ninf(), l = 0.0f, acc[N] = {};
   const bool mine = lane * N < D;
@@ -713,7 +753,7 @@ __global__ __launch_bounds__(256) void k_attend_rows_join(AttendArgs a) {
   const Row row = row_of(a, t, a.s.len(info.b), t.first + r);
   const bool some = row.hi > row.lo;
   const float inv = some ? 1.0f / l : 0.0f;
-  const uint32_t h = info.head * a.group + row.head;
+  const uint32_t h = (info.head * a.wg_heads + blockIdx.z) * a.group + row.head;
   TI *out = static_cast<TI *>(a.out) + (uint64_t)row.token * a.out_stride + (uint64_t)h * D;
   if (threadIdx.x < D / 2) {
     const uint32_t x = threadIdx.x * 2;
@@ -1104,6 +1144,7 @@ __global__ __launch_bounds__(256) void k_attend_tile_join(AttendArgs a) {
 struct Plan {
   uint32_t rows;      // 16 or 128 to a workgroup
   uint32_t grid;      // workgroups of the 16-row kernel
+  uint32_t wg_heads;  // KV heads to one of them
   bool whole, join;   // it cuts no row tile; a second launch is needed
   bool by_unit;       // JoinInfo records: one for each row tile and KV head
   uint64_t infos;
@@ -1116,10 +1157,11 @@ struct Plan {
 constexpr uint32_t kCus = 256;
 constexpr uint32_t resident(uint32_t head_dim) { return (head_dim == 256 ? 1 : 2) * kCus; }
 
-// A 16-row workgroup takes at least this many steps: one for each wave.
-constexpr uint32_t kMinSteps = 4;
 // Caches of at most this many steps are not cut.
 constexpr uint32_t kWholeSteps = 16;
+
+// A 16-row workgroup takes at least a step for each wave of a head.
+uint32_t min_steps(const Plan &w) { return 4 / w.wg_heads; }
 
 Plan make_plan(const kvc_paged_desc &p, const kvc_paged_batch &b) {
   Plan w{};
@@ -1132,7 +1174,9 @@ Plan make_plan(const kvc_paged_desc &p, const kvc_paged_batch &b) {
   w.tiles = b.q_start ? (uint32_t)((uint64_t)b.n_tokens * group / w.rows) +
                             std::min(b.n_seqs, b.n_tokens)
                       : b.n_seqs * ((group + 15) / 16);
-  const uint64_t units = (uint64_t)w.tiles * p.n_kv_heads;
+  w.wg_heads = p.n_kv_heads % 4 == 0 ? 4 : p.n_kv_heads % 2 == 0 ? 2 : 1;
+  if (w.rows == 128) w.wg_heads = 1;
+  const uint64_t units = (uint64_t)w.tiles * (p.n_kv_heads / w.wg_heads);
   uint64_t parts = 0;
   if (w.rows == 16) {
     uint64_t steps = std::max<uint64_t>(1, ((uint64_t)b.max_len + kTok - 1) / kTok);
@@ -1146,11 +1190,11 @@ Plan make_plan(const kvc_paged_desc &p, const kvc_paged_batch &b) {
       // each row tile once; a batch of single tokens needs no search for it
       w.grid = (uint32_t)(b.q_start ? std::min<uint64_t>(units, 4 * slots) : units);
     } else {
-      w.grid = (uint32_t)std::min<uint64_t>(slots, (units * steps + kMinSteps - 1) / kMinSteps);
+      w.grid = (uint32_t)std::min<uint64_t>(slots, (units * steps + min_steps(w) - 1) / min_steps(w));
       w.join = true;
       w.by_unit = !b.q_start && units < w.grid;
       w.infos = w.by_unit ? units : w.grid;
-      parts = 2ull * w.grid;
+      parts = 2ull * w.grid * w.wg_heads;
     }
   } else {
     // Equal splits of every row tile: as many as make the workgroups come out
@@ -1180,7 +1224,8 @@ hipError_t launch_d(const AttendArgs &a, const Plan &w, hipStream_t stream) {
     if (w.join)
       hipLaunchKernelGGL((k_attend_rows_join<TI, TC, D>),
                          dim3((uint32_t)w.infos, a.s.q_start ? kRowTile
-                                                             : std::min(kRowTile, a.group)),
+                                                             : std::min(kRowTile, a.group),
+                              w.wg_heads),
                          dim3(256), 0, stream, a);
   } else {
     hipLaunchKernelGGL((k_attend_tile<TI, TC, D>), dim3(units * w.splits), dim3(256), kBigLds<D>,
@@ -1217,7 +1262,9 @@ hipError_t launch_attend(const kvc_paged_desc &p, const kvc_paged_batch &b, Atte
   a.step_shift = w.shift;
   a.by_unit = w.by_unit;
   a.pieces = w.grid;
-  a.min_steps = kMinSteps;
+  a.min_steps = min_steps(w);
+  a.wg_heads = w.wg_heads;
+  a.head_groups = a.n_kv_heads / w.wg_heads;
   uint8_t *base = static_cast<uint8_t *>(ws);
   a.part = reinterpret_cast<float *>(base + w.part);
   a.part_ml = reinterpret_cast<float *>(base + w.part_ml);

@@ -136,6 +136,8 @@ struct AttendArgs {
   uint32_t step_shift;  // log2 of the tokens of a step of the 16-row kernel, at least 5
   uint32_t min_steps;  // of the 16-row kernel: steps a workgroup takes at least
   uint32_t pieces;     // its workgroups
+  uint32_t wg_heads;   // KV heads to one of them (1, 2 or 4)
+  uint32_t head_groups;
   bool by_unit;        // the layout of its join records
   bool whole;          // the 16-row kernel cuts no row tile
   float scale;      // scale * log2(e)

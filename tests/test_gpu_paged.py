@@ -126,6 +126,10 @@ SINGLE = [
     (6, 3, 64, 10, BF16, BF16, [(i * 13) % 29 * 17 for i in range(520)], 0),
     (3, 1, 96, 16, F16, F16, [2000] + [0] * 260 + [1500, 1, 600], 900),
     (20, 1, 128, 16, BF16, F16, [1100, 513, 2300], 0),
+    # two and four KV heads side by side, groups that pass a row tile
+    (12, 6, 64, 16, F16, F16, [700, 33, 1025, 0, 2], 0),
+    (68, 4, 96, 7, BF16, BF16, [640, 800, 31], 500),
+    (8, 8, 256, 16, F16, F16, [900, 513], 0),
 ]
 
 
@@ -150,6 +154,7 @@ PROMPT = [
     (8, 2, 64, 16, F16, F16, [900, 1500, 30, 700, 5], [9, 3, 30, 0, 1], 0),
     (6, 1, 128, 20, BF16, BF16, [1201, 33, 0, 640], [17, 5, 0, 2], 300),
     (40, 2, 256, 16, BF16, F16, [800, 513], [3, 2], 0),
+    (4, 4, 128, 16, BF16, F16, [1300, 700, 90], [20, 3, 40], 0),
     # 128-row tiles: a split context, no grouping, a group of 7 and of 128, windows
     (8, 2, 128, 16, F16, F16, [2050], [40], 0),
     (2, 2, 128, 64, BF16, BF16, [257, 700], [257, 129], 0),
