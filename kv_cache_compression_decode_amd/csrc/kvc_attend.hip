@@ -182,6 +182,9 @@ __device__ inline Row row_of(const AttendArgs &a, const Tile &t, int32_t len, ui
 //
 // Where no cache is longer than a few steps (`whole`), every row tile counts
 // as one step, is never cut, and needs no join.
+// Workgroups that the 256 CUs hold at once (by registers): the pieces at most.
+constexpr uint32_t kCus = 256;
+constexpr uint32_t resident(uint32_t head_dim) { return (head_dim == 256 ? 1 : 2) * kCus; }
 constexpr uint32_t kRowTile = 16;
 constexpr uint32_t kTok = 32;
 
@@ -692,14 +695,18 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
 }
 
 // Joins the parts of a row tile that k_attend_rows cut: a workgroup for each
-// JoinInfo, row and head of the group.  Four waves share the parts and are added up through LDS
-// in a fixed order.
-template <class TI, class TC, int D>
-__global__ __launch_bounds__(256) void k_attend_rows_join(AttendArgs a) {
+// JoinInfo, row and head of the group.  Its W waves share the parts and are
+// added up through LDS in a fixed order: 16 waves where there are few rows to
+// join and so many parts to each, 4 otherwise.
+template <class TI, class TC, int D, uint32_t W>
+__global__ __launch_bounds__(W * 64) void k_attend_rows_join(AttendArgs a) {
   constexpr int N = D > 128 ? 4 : D > 64 ? 2 : 1;  // dimensions a lane
-  __shared__ float s_acc[4][D];
+  constexpr uint32_t kParts = 2 * kCus;  // parts at most
+  constexpr uint32_t M = (kParts + W * 64 - 1) / (W * 64);
+  __shared__ float s_acc[W][D], s_f[kParts], s_m[W], s_l[W];
   const JoinInfo info = static_cast<const JoinInfo *>(a.info)[blockIdx.x];
-  if (info.cut != 1 || info.b >= a.s.n_seqs || info.last >= a.pieces) return;
+  if (info.cut != 1 || info.b >= a.s.n_seqs || info.first > info.last || info.last >= a.pieces)
+    return;
   const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = blockIdx.y;
   uint32_t row0, n;
   a.s.rows(info.b, row0, n);
@@ -710,47 +717,69 @@ __global__ __launch_bounds__(256) void k_attend_rows_join(AttendArgs a) {
   auto part_of = [&](uint32_t i) {
     return ((uint64_t)(info.first + i) * 2 + (i == 0 ? info.slot : 0)) * a.wg_heads + blockIdx.z;
   };
-  float mm = ninf(), l = 0.0f, acc[N] = {};
+  // Everything is asked for before anything is waited for: the parts' maxima
+  // and sums, a thread each, and each wave's first eight parts.
+  float m[M], ls[M];
+#pragma unroll
+  for (uint32_t j = 0; j < M; ++j) {
+    const uint32_t i = threadIdx.x + j * W * 64, ic = min(i, parts - 1);
+    m[j] = a.part_ml[part_of(ic) * 32 + r];
+    ls[j] = a.part_ml[part_of(ic) * 32 + 16 + r];
+    if (i >= parts) m[j] = ninf();
+  }
   const bool mine = lane * N < D;
-  for (uint32_t i = lane; i < parts; i += 64)
-    mm = __builtin_fmaxf(mm, a.part_ml[part_of(i) * 32 + r]);
+  float x[8][N], acc[N] = {};
+  auto load8 = [&](uint32_t i) {  // past the last one: the last one, unused
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float *op = a.part + (part_of(min(i + j * W, parts - 1)) * 16 + r) * D + lane * N;
+#pragma unroll
+      for (int e = 0; e < N; ++e) x[j][e] = mine ? op[e] : 0.0f;
+    }
+  };
+  if (wave < parts) load8(wave);
+  const int32_t len = a.s.len(info.b);
+  float mm = m[0];
+#pragma unroll
+  for (uint32_t j = 1; j < M; ++j) mm = __builtin_fmaxf(mm, m[j]);
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) mm = __builtin_fmaxf(mm, __shfl_xor(mm, d));
+  s_m[wave] = mm;
+  __syncthreads();
+#pragma unroll
+  for (uint32_t w = 0; w < W; ++w) mm = __builtin_fmaxf(mm, s_m[w]);
   const float ref = mm == ninf() ? 0.0f : mm;
-  for (uint32_t i0 = 0; i0 < parts; i0 += 64) {
-    float f = 0.0f;
-    if (i0 + lane < parts) {
-      const uint64_t p = part_of(i0 + lane);
-      f = __builtin_amdgcn_exp2f(a.part_ml[p * 32 + r] - ref);
-      l = __builtin_fmaf(a.part_ml[p * 32 + 16 + r], f, l);
-    }
-    const uint32_t here = min(64u, parts - i0);
-    // eight parts' loads in flight; past the last one: the last one, unused
-    for (uint32_t i = wave; i < here; i += 32) {
-      float fi[8], x[8][N];
+  float l = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t ij = i + j * 4, ic = min(ij, here - 1);
-        const float fc = __shfl(f, (int)ic);
-        fi[j] = ij < here ? fc : 0.0f;
-        const float *op = a.part + (part_of(i0 + ic) * 16 + r) * D + lane * N;
-#pragma unroll
-        for (int e = 0; e < N; ++e) x[j][e] = mine ? op[e] : 0.0f;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-          acc[e] = fi[j] == 0.0f ? acc[e] : __builtin_fmaf(x[j][e], fi[j], acc[e]);
+  for (uint32_t j = 0; j < M; ++j) {
+    const uint32_t i = threadIdx.x + j * W * 64;
+    const float f = __builtin_amdgcn_exp2f(m[j] - ref);
+    if (i < parts) {
+      s_f[i] = f;
+      l = __builtin_fmaf(ls[j], f, l);
     }
   }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
+  s_l[wave] = l;
+  __syncthreads();
+  for (uint32_t i = wave; i < parts; i += 8 * W) {
+    if (i != wave) load8(i);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float f = i + j * W < parts ? s_f[i + j * W] : 0.0f;
+#pragma unroll
+      for (int e = 0; e < N; ++e) acc[e] = f == 0.0f ? acc[e] : __builtin_fmaf(x[j][e], f, acc[e]);
+    }
+  }
   if (mine)
 #pragma unroll
     for (int e = 0; e < N; ++e) s_acc[wave][lane * N + e] = acc[e];
   __syncthreads();
-  const Row row = row_of(a, t, a.s.len(info.b), t.first + r);
+  l = 0.0f;
+#pragma unroll
+  for (uint32_t w = 0; w < W; ++w) l += s_l[w];
+  const Row row = row_of(a, t, len, t.first + r);
   const bool some = row.hi > row.lo;
   const float inv = some ? 1.0f / l : 0.0f;
   const uint32_t h = (info.head * a.wg_heads + blockIdx.z) * a.group + row.head;
@@ -759,7 +788,7 @@ __global__ __launch_bounds__(256) void k_attend_rows_join(AttendArgs a) {
     const uint32_t x = threadIdx.x * 2;
     float v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (uint32_t w = 0; w < W; ++w) {
       v0 += s_acc[w][x];
       v1 += s_acc[w][x + 1];
     }
@@ -1153,10 +1182,6 @@ struct Plan {
   uint64_t part, part_ml, info, total;  // workspace offsets
 };
 
-// Workgroups that the 256 CUs hold at once (by registers).
-constexpr uint32_t kCus = 256;
-constexpr uint32_t resident(uint32_t head_dim) { return (head_dim == 256 ? 1 : 2) * kCus; }
-
 // Caches of at most this many steps are not cut.
 constexpr uint32_t kWholeSteps = 16;
 
@@ -1221,12 +1246,14 @@ hipError_t launch_d(const AttendArgs &a, const Plan &w, hipStream_t stream) {
       hipLaunchKernelGGL((k_attend_rows<TI, TC, D, false>), dim3(w.grid), dim3(256), 0, stream, a);
     else
       hipLaunchKernelGGL((k_attend_rows<TI, TC, D, true>), dim3(w.grid), dim3(256), 0, stream, a);
-    if (w.join)
-      hipLaunchKernelGGL((k_attend_rows_join<TI, TC, D>),
-                         dim3((uint32_t)w.infos, a.s.q_start ? kRowTile
-                                                             : std::min(kRowTile, a.group),
-                              w.wg_heads),
-                         dim3(256), 0, stream, a);
+    if (w.join) {
+      const dim3 grid((uint32_t)w.infos, a.s.q_start ? kRowTile : std::min(kRowTile, a.group),
+                      w.wg_heads);
+      if ((uint64_t)grid.x * grid.y * grid.z <= 2 * kCus)
+        hipLaunchKernelGGL((k_attend_rows_join<TI, TC, D, 16>), grid, dim3(1024), 0, stream, a);
+      else
+        hipLaunchKernelGGL((k_attend_rows_join<TI, TC, D, 4>), grid, dim3(256), 0, stream, a);
+    }
   } else {
     hipLaunchKernelGGL((k_attend_tile<TI, TC, D>), dim3(units * w.splits), dim3(256), kBigLds<D>,
                        stream, a);
