@@ -16,6 +16,22 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 __device__ inline u32x4 load16(const void *p) { return *reinterpret_cast<const u32x4 *>(p); }
 __device__ inline void store16(void *p, u32x4 v) { *reinterpret_cast<u32x4 *>(p) = v; }
 
+// The same, past the caches if kStream (non-temporal).  Calls that move more
+// than kStreamBytes, which the caches (256 MB) would not hold until the next
+// reader anyway, use it.
+constexpr uint64_t kStreamBytes = 256ull << 20;
+template <bool kStream>
+__device__ inline u32x4 move_load(const void *p) {
+  return kStream ? __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p)) : load16(p);
+}
+template <bool kStream>
+__device__ inline void move_store(void *p, u32x4 v) {
+  if (kStream)
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(p));
+  else
+    store16(p, v);
+}
+
 // The two elements of a dword, widened (both types widen exactly).
 template <class T>
 __device__ inline float elem_lo(uint32_t w);

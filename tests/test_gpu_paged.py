@@ -298,6 +298,51 @@ def test_append(heads, kv_heads, head_dim, page, io, cache, lens, new, rotary, i
     assert torch.equal(q_out[a:], q0[a:] if in_place else torch.full_like(q_out[a:], 7.0))
 
 
+@pytest.mark.parametrize("inter", [False, True])
+def test_append_beyond_the_caches(inter):
+    """A call that moves more than 256 MB (287 MB here) goes past the caches:
+    the same bits as the same tokens in calls of a third."""
+    n = 7002
+    st = Setup([n + 5], [n], 64, 8, 128, 16, BF16, F16, layers=2)
+    rope = kvc.Rope(kvc.rope_table(n + 5, 128, device=DEV), interleaved=inter)
+    q_out = torch.zeros_like(st.q.contiguous())
+    kvc.append_async(st.desc, st.batch, 1, st.pool, st.k, st.v, st.wsp, rope=rope, q=st.q,
+                     q_out=q_out)
+    kvc.read_status(st.wsp.status, "append")
+    pool, q2 = st.pool.clone(), torch.zeros_like(q_out)
+    pool[1][:, st.slots(0)[5:]] = 0
+    for a in range(0, n, n // 3):
+        rows = slice(a, a + n // 3)
+        st.lens.fill_(5 + a + n // 3)
+        part = kvc.PagedBatch(st.table, st.lens, max_len=n + 5,
+                              q_start=torch.tensor([0, n // 3], dtype=torch.int32, device=DEV))
+        kvc.append_async(st.desc, part, 1, pool, st.k[rows], st.v[rows], st.wsp, rope=rope,
+                         q=st.q[rows], q_out=q2[rows])
+    kvc.read_status(st.wsp.status, "append")
+    assert torch.equal(pool.view(torch.int16), st.pool.view(torch.int16))
+    assert torch.equal(q2, q_out)
+
+
+def test_page_moves_beyond_the_caches():
+    layers, n, page, c = 9, 4001, 20, 1024  # 295 MB read and written
+    g = _gen(8)
+    n_pages = 210
+    desc = kvc.make_paged_desc(layers, 8, 8, 128, page, n_pages)
+    pool = torch.randn(desc.pool_shape, generator=g, device=DEV).to(F16)
+    table = torch.randperm(n_pages, generator=g, device=DEV).to(torch.int32)
+    s = ref.slots(table, n + 3, page, DEV)[3:]
+    flat = torch.zeros((layers, 2, n + 1, c), dtype=F16, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    kvc.page_out_async(desc, pool, table, 3, n, flat, 1, status)
+    assert torch.equal(flat[:, :, 1:], pool[:, :, s]) and bool((flat[:, :, 0] == 0).all())
+    flat.neg_()
+    want = pool.clone()
+    want[:, :, s] = flat[:, :, 1:]
+    kvc.page_in_async(desc, flat, 1, pool, table, 3, n, status)
+    assert torch.equal(pool, want)
+    kvc.read_status(status, "pages")
+
+
 def test_append_padding_and_keys_only():
     """Rows of negative position are skipped; q may be left out."""
     st = Setup([0, 5, 0], [1, 1, 1], 4, 2, 64, 16, F16, F16, single=True)
