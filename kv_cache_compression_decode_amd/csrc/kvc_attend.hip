@@ -61,7 +61,7 @@ __device__ inline float ninf() { return -__builtin_inff(); }
 // probability instead of 2^-24, so a long tail of small ones is not lost.
 template <class T>
 constexpr float kShift = std::is_same<T, f16>::value ? 14.0f : 0.0f;
-// In the kernel of 128 rows a probability may pass 1 by 2^kGrow before the
+// In the kernel for prompts a probability may pass 1 by 2^kGrow before the
 // sums are rescaled, and binary16 holds less than 2^16.
 constexpr float kGrow = 4.0f;
 template <class T>
@@ -799,41 +799,57 @@ __global__ __launch_bounds__(W * 64) void k_attend_rows_join(AttendArgs a) {
         some ? (mm - kShift<TC> + __builtin_amdgcn_logf(l)) * kLn2 : ninf();
 }
 
-// ------------------------------------------------------ 128 rows a workgroup
-// For prompts: four waves of 32 rows each share tiles of 64 tokens in LDS (32
-// where head_dim is 256), so
-// a key or value is fetched once for 128 rows.  Scores are transposed here
-// too (S^T = K Q^T on 32 x 32 tiles): a lane holds half a row's scores, the
-// other half of the row in lane ^ 32, so a row's maximum is a chain in one
-// lane and one exchange, and P^T is again the second operand of O^T = V^T P^T
-// without leaving its lane.  V^T comes from LDS through the transposing read,
-// four tokens of a dimension at a time.
+// ----------------------------------------------- 128 or 256 rows a workgroup
+// For prompts: NW waves of 32 rows each share tiles of 64 tokens in LDS (32
+// where head_dim is 256), so a key or value is fetched once for all of them.
+// Scores are transposed here too (S^T = K Q^T on 32 x 32 tiles): a lane holds
+// half a row's scores, the other half of the row in lane ^ 32, so a row's
+// maximum is a chain in one lane and one exchange, and P^T is again the second
+// operand of O^T = V^T P^T without leaving its lane.  V^T comes from LDS
+// through the transposing read, four tokens of a dimension at a time.
 //
-// Tiles are double-buffered: the next one is loaded to registers while this
-// one is multiplied, then stored to the other buffer: one barrier a tile.
-// Rows of K are padded by 16 bytes, so that 16-byte reads of eight rows (or
-// sixteen) fall into different banks, rows of V by 32, so that the four rows
-// of a transposing read do.
+// The next tile is loaded to registers among the products of this one's
+// scores (in a burst the eight waves' loads would stall each other) and
+// stored to the other buffer at the step's end: one barrier a tile.  Rows of
+// K are padded by 16 bytes, so that 16-byte reads of 16 rows fall into
+// different banks, rows of V to 64 or 192 bytes mod 256, so that the four rows
+// of a transposing read do (no conflict left; with V padded by 32 bytes they
+// were a quarter of the LDS's busy cycles).
+//
+// The matrix and the vector unit can work at the same time, for different
+// waves.  The two waves of a SIMD leave a barrier together, so the waves from
+// the fourth on (late) put off a tile's second product to the next step's
+// beginning, while the others are in their first: values have three buffers
+// for that (2% faster).  Software pipelining inside a wave (the next tile's
+// scores among this one's exponentials) was slower, 13%: the registers that
+// it holds are missing for LDS reads ahead of the matrix unit.
 //
 // The sums are rescaled only when some row of the wave grew by more than
 // kGrow binary orders since its reference was set.
-constexpr uint32_t kBigRows = 128;
+//
+// 256 rows against 128: five prompts over long contexts (1.55 TFLOP) 1.63
+// against 1.79 ms.
 template <int D>
 constexpr uint32_t kBigTok = D == 256 ? 32 : 64;  // 32: a tile's registers would not fit
 template <int D>
 constexpr uint32_t kKeyStride = D * 2 + 16;
 template <int D>
-constexpr uint32_t kValStride = D * 2 + 32;
+constexpr uint32_t kValStride = D * 2 + (D == 96 ? 0 : 64);
 template <int D>
-constexpr uint32_t kBigBuf = kBigTok<D> * (kKeyStride<D> + kValStride<D>);
+constexpr uint32_t kKeyBuf = kBigTok<D> * kKeyStride<D>;
 template <int D>
-constexpr uint32_t kBigLds = 2 * kBigBuf<D> + 32;
+constexpr uint32_t kValBuf = kBigTok<D> * kValStride<D>;
+constexpr int val_bufs(int waves) { return waves == 8 ? 3 : 2; }
+template <int D, int NW>
+constexpr uint32_t kBigLds = 2 * kKeyBuf<D> + val_bufs(NW) * kValBuf<D> + 32;
+__device__ inline uint32_t next_odd_of(uint32_t i) { return i == 2 ? 0 : i + 1; }
 
 // Row tile `t` of the call: the sequences in order, of each its last tile (the
 // one with the most visible tokens) first, so that a launch ends with short
 // ones (6,001 tokens from the first on: a fifth less time).  Each wave
 // finds it by itself: 64 sequences at a time, a scan of their tile counts.
 // False if the batch has fewer tiles.
+template <uint32_t kRows>
 __device__ inline bool find_tile(const AttendArgs &a, uint32_t t, Tile &out) {
   const uint32_t lane = threadIdx.x & 63;
   uint32_t base = 0;
@@ -844,7 +860,7 @@ __device__ inline bool find_tile(const AttendArgs &a, uint32_t t, Tile &out) {
       a.s.rows(b, row0, n);
       if (t == 0 && a.s.rows_bad(b)) set_status(a.status, KVC_ERR_SHAPE);
     }
-    const uint32_t mine = (n * a.group + kBigRows - 1) / kBigRows;
+    const uint32_t mine = (n * a.group + kRows - 1) / kRows;
     uint32_t sum = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -858,10 +874,10 @@ __device__ inline bool find_tile(const AttendArgs &a, uint32_t t, Tile &out) {
       out.row0 = __shfl(row0, src);
       out.n = __shfl(n, src);
       const uint32_t k = t - base - __shfl(sum - mine, src);
-      const uint32_t tiles = (out.n * a.group + kBigRows - 1) / kBigRows;
+      const uint32_t tiles = (out.n * a.group + kRows - 1) / kRows;
       if (k >= tiles) return false;  // only if q_start overlaps itself
-      out.first = (tiles - 1 - k) * kBigRows;
-      out.rows = min(kBigRows, out.n * a.group - out.first);
+      out.first = (tiles - 1 - k) * kRows;
+      out.rows = min(kRows, out.n * a.group - out.first);
       return true;
     }
     base += __shfl(sum, 63);
@@ -869,23 +885,26 @@ __device__ inline bool find_tile(const AttendArgs &a, uint32_t t, Tile &out) {
   return false;
 }
 
-template <class TI, class TC, int D>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_tile(AttendArgs a) {
+template <class TI, class TC, int D, int NW>
+__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tile(AttendArgs a) {
   constexpr int TOK = kBigTok<D>, HT = TOK / 32;
+  constexpr uint32_t kThreads = NW * 64, kRows = NW * 32;
+  constexpr int VB = val_bufs(NW);
   constexpr int KK = D / 16;        // steps of the first product
   constexpr int DT = D / 32;        // dimension tiles of the second
   constexpr int CH = D / 8;         // 16-byte vectors of a row
-  constexpr int TT = 256 / TOK;     // threads to a token
-  constexpr int NC = CH / TT;       // vectors each moves
+  constexpr int TT = kThreads / TOK;  // threads to a token
+  constexpr int NC = (CH + TT - 1) / TT;  // vectors each moves at most
   extern __shared__ __align__(16) uint8_t lds[];
-  uint32_t *s_odd = reinterpret_cast<uint32_t *>(lds + 2 * kBigBuf<D>);  // [3][2]
+  uint8_t *const s_val = lds + 2 * kKeyBuf<D>;
+  uint32_t *const s_odd = reinterpret_cast<uint32_t *>(s_val + VB * kValBuf<D>);  // [3][2]
   const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const uint32_t n32 = lane & 31, hi = lane >> 5;
   const uint32_t hk = blockIdx.x % a.n_kv_heads;
   const uint32_t rest = blockIdx.x / a.n_kv_heads;
   const uint32_t split = rest % a.splits, tile = rest / a.splits;
   Tile t;
-  if (!find_tile(a, tile, t)) return;
+  if (!find_tile<kRows>(a, tile, t)) return;
   const int32_t len = a.s.len(t.b);
   if (threadIdx.x == 0 && a.s.len_bad(t.b)) set_status(a.status, KVC_ERR_SHAPE);
   const uint32_t w0 = wave * 32;
@@ -937,39 +956,75 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_tile(AttendArg
     next_id = (uint32_t)table[page];
     next_in = (uint32_t)j - page * a.s.page.d;
   };
+  auto mine = [&](int i) { return CH % TT == 0 || my_c + TT * i < (uint32_t)CH; };
   auto load_tile = [&]() {
     uint32_t slot;
     bad = !a.s.slot_in(next_id, next_in, slot) || bad;
     const TC *kp = kmine + (uint64_t)slot * a.row;
     const TC *vp = kp + k_to_v;
 #pragma unroll
-    for (int i = 0; i < NC; ++i) kr[i] = load16(kp + i * TT * 8);
+    for (int i = 0; i < NC; ++i)
+      if (mine(i)) kr[i] = load16(kp + i * TT * 8);
 #pragma unroll
-    for (int i = 0; i < NC; ++i) vr[i] = load16(vp + i * TT * 8);
+    for (int i = 0; i < NC; ++i)
+      if (mine(i)) vr[i] = load16(vp + i * TT * 8);
   };
   // Hidden tokens of a value tile must not meet the second product with an
   // infinity or NaN (0 times it is NaN): tokens past the end are zeroed, and
   // a token that some rows see and others do not is noted in s_odd.
   auto store_tile = [&](int32_t ti, uint32_t odd_at) {
     const int32_t j0 = begin + ti * TOK;
-    uint8_t *kb = lds + (ti & 1) * kBigBuf<D>, *vb = kb + TOK * kKeyStride<D>;
+    uint8_t *kb = lds + (ti & 1) * kKeyBuf<D>;
+    uint8_t *vb = s_val + (VB == 3 ? odd_at : ti & 1) * kValBuf<D>;
     if (j0 < r_last.lo || j0 + TOK > r_first.hi) {
       bool nf = false;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         if (j0 + (int32_t)my_t >= end) vr[i] = u32x4{0, 0, 0, 0};
+        if (mine(i))
 #pragma unroll
-        for (int w = 0; w < 4; ++w) nf = nf || nonfinite2<TC>(vr[i][w]);
+          for (int w = 0; w < 4; ++w) nf = nf || nonfinite2<TC>(vr[i][w]);
       }
       if (nf) atomicOr(&s_odd[odd_at * 2 + (my_t >> 5)], 1u << (my_t & 31));
     }
     kb += my_t * kKeyStride<D> + my_c * 16;
     vb += my_t * kValStride<D> + my_c * 16;
 #pragma unroll
-    for (int i = 0; i < NC; ++i) store16(kb + i * TT * 16, kr[i]);
+    for (int i = 0; i < NC; ++i)
+      if (mine(i)) store16(kb + i * TT * 16, kr[i]);
 #pragma unroll
-    for (int i = 0; i < NC; ++i) store16(vb + i * TT * 16, vr[i]);
+    for (int i = 0; i < NC; ++i)
+      if (mine(i)) store16(vb + i * TT * 16, vr[i]);
   };
+
+  // O^T += V^T P^T with the values at vb.  Lane l reads token (l%16)/4 (+ 4 for
+  // the upper half), dimensions (l/16%2)*16 + (l%4)*4 .. +3 and receives four
+  // tokens of dimension l%32.
+  u32x4 pf[2 * HT];
+  auto values = [&](const uint8_t *vb) {
+    const uint8_t *vp = vb + (hi * 4 + ((lane & 15) >> 2)) * kValStride<D> +
+                        ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int st = 0; st < 2 * HT; ++st)
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        const uint8_t *p0 = vp + st * 16 * kValStride<D> + d * 64;
+        const u32x2 v0 = read_tr(p0), v1 = read_tr(p0 + 8 * kValStride<D>);
+        o[d] = mfma32<TC>(u32x4{v0[0], v0[1], v1[0], v1[1]}, pf[st], o[d]);
+      }
+    // two products' operands ahead
+    __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+    for (int i = 0; i < 2 * HT * DT - 2; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);
+    __builtin_amdgcn_s_setprio(0);
+  };
+  const bool late = VB == 3 && wave >= 4;
+  bool pending = false;  // pf waits for its values
 
   if (threadIdx.x < 6) s_odd[threadIdx.x] = 0;
   uint32_t odd_at = 0;  // of the tile being multiplied: its number mod 3
@@ -983,23 +1038,26 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_tile(AttendArg
   }
   for (int32_t ti = t_lo; ti < t_hi; ++ti) {
     const int32_t j0 = begin + ti * TOK;
-    uint8_t *kb = lds + (ti & 1) * kBigBuf<D>, *vb = kb + TOK * kKeyStride<D>;
+    uint8_t *kb = lds + (ti & 1) * kKeyBuf<D>;
+    uint8_t *vb = s_val + (VB == 3 ? odd_at : ti & 1) * kValBuf<D>;
     const bool more = ti + 1 < t_hi;
-    if (more) load_tile();
-    if (ti + 2 < t_hi) look_up(ti + 2);
-    const uint32_t next_odd = odd_at == 2 ? 0 : odd_at + 1;
+    const uint32_t next_odd = next_odd_of(odd_at);
     uint64_t odd = 0;
     // the slot that tile ti + 2 will use: last read a barrier ago
-    if (threadIdx.x < 2) s_odd[(next_odd == 2 ? 0 : next_odd + 1) * 2 + threadIdx.x] = 0;
+    if (threadIdx.x < 2) s_odd[next_odd_of(next_odd) * 2 + threadIdx.x] = 0;
     if (j0 < r_last.lo || j0 + TOK > r_first.hi) {
       odd = s_odd[odd_at * 2] | (uint64_t)s_odd[odd_at * 2 + 1] << 32;
       if (odd) {
         __syncthreads();  // every wave has read the mask
-        for (uint32_t i = threadIdx.x; i < (uint32_t)(TOK * CH); i += 256)
+        for (uint32_t i = threadIdx.x; i < (uint32_t)(TOK * CH); i += kThreads)
           if ((odd >> (i / CH)) & 1)
             store16(vb + (i / CH) * kValStride<D> + (i % CH) * 16, u32x4{0, 0, 0, 0});
         __syncthreads();
       }
+    }
+    if (late && pending) {  // of the tile before, two words of s_odd on
+      values(s_val + next_odd_of(next_odd) * kValBuf<D>);
+      pending = false;
     }
     // a wave has nothing to do where none of its rows sees a token
     if (busy && j0 < w_last.hi && j0 + TOK > w_first.lo) {
@@ -1014,13 +1072,17 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_tile(AttendArg
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) s[h] = mfma32<TC>(load16(kp + kk * 32), qf[kk], s[h]);
       }
-      {
-        constexpr int total = HT * KK, depth = 4;
+      // past the last tile these load the last token again
+      load_tile();
+      look_up(ti + 2);
+      {  // four keys ahead of the matrix unit, the loads spread out
+        constexpr int total = HT * KK, depth = 4, gap = std::max(1, (total - depth) / (2 * NC + 1));
         __builtin_amdgcn_sched_group_barrier(0x100, depth, 0);
 #pragma unroll
         for (int i = 0; i < total - depth; ++i) {
           __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
           __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          if (i % gap == gap - 1) __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
         }
         __builtin_amdgcn_sched_group_barrier(0x8, depth, 0);
       }
@@ -1076,40 +1138,23 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_tile(AttendArg
               o[d][i] = __builtin_fmaf(pj, (float)vp[d * 32 + (i >> 2) * 8 + (i & 3)], o[d][i]);
         }
       }
-      // lane l reads token (l%16)/4 (+ 4 for the upper half), dimensions
-      // (l/16%2)*16 + (l%4)*4 .. +3 and receives four tokens of dimension l%32
-      const uint8_t *vp = vb + (hi * 4 + ((lane & 15) >> 2)) * kValStride<D> +
-                          ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
-      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int st = 0; st < TOK / 16; ++st) {
-        u32x4 pf;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          pf[i] = pack2<TC>(s[st >> 1][(st & 1) * 8 + 2 * i], s[st >> 1][(st & 1) * 8 + 2 * i + 1]);
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          const uint8_t *p0 = vp + st * 16 * kValStride<D> + d * 64;
-          const u32x2 v0 = read_tr(p0), v1 = read_tr(p0 + 8 * kValStride<D>);
-          o[d] = mfma32<TC>(u32x4{v0[0], v0[1], v1[0], v1[1]}, pf, o[d]);
-        }
-      }
-      {
-        constexpr int total = TOK / 16 * DT, depth = 2;
-        __builtin_amdgcn_sched_group_barrier(0x100, 2 * depth, 0);
-#pragma unroll
-        for (int i = 0; i < total - depth; ++i) {
-          __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-        }
-        __builtin_amdgcn_sched_group_barrier(0x8, depth, 0);
-      }
+      for (int i = 0; i < 8 * HT; ++i)
+        pf[i >> 2][i & 3] = pack2<TC>(s[i >> 3][2 * i & 15], s[i >> 3][(2 * i & 15) + 1]);
+      pending = true;
+    } else {
+      load_tile();
+      look_up(ti + 2);
     }
-    __builtin_amdgcn_s_setprio(0);
+    if (!late && pending) {
+      values(vb);
+      pending = false;
+    }
     if (more) store_tile(ti + 1, next_odd);
     odd_at = next_odd;
     __syncthreads();
   }
+  if (late && pending) values(s_val + next_odd_of(next_odd_of(odd_at)) * kValBuf<D>);
   if (__ballot(bad) && lane == 0) set_status(a.status, KVC_ERR_SHAPE);
   l += other_half(l);
   if (!live) return;
@@ -1132,7 +1177,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_tile(AttendArg
           some ? (ref - kShiftBig<TC> + __builtin_amdgcn_logf(l)) * kLn2 : ninf();
   } else {
     const uint64_t part = ((uint64_t)tile * a.n_kv_heads + hk) * a.splits + split;
-    float *op = a.part + (part * kBigRows + w0 + n32) * D + hi * 4;
+    float *op = a.part + (part * kRows + w0 + n32) * D + hi * 4;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -1140,22 +1185,21 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_tile(AttendArg
         *reinterpret_cast<f32x4 *>(op + d * 32 + i * 8) =
             f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
     if (hi == 0) {
-      a.part_ml[part * (2 * kBigRows) + w0 + n32] = ref;
-      a.part_ml[part * (2 * kBigRows) + kBigRows + w0 + n32] = l;
+      a.part_ml[part * (2 * kRows) + w0 + n32] = ref;
+      a.part_ml[part * (2 * kRows) + kRows + w0 + n32] = l;
     }
   }
 }
 
 // Joins the splits of k_attend_tile: a wave per (row tile, KV head, row).
-template <class TI, class TC, int D>
+template <class TI, class TC, int D, uint32_t kRows>
 __global__ __launch_bounds__(256) void k_attend_tile_join(AttendArgs a) {
-  constexpr uint32_t kRows = kBigRows;
   const uint32_t lane = threadIdx.x & 63;
   const uint32_t unit = blockIdx.x / (kRows / 4);
   const uint32_t r = (blockIdx.x % (kRows / 4)) * 4 + (threadIdx.x >> 6);
   const uint32_t hk = unit % a.n_kv_heads, tile = unit / a.n_kv_heads;
   Tile t;
-  if (!find_tile(a, tile, t)) return;
+  if (!find_tile<kRows>(a, tile, t)) return;
   if (r >= t.rows) return;
   const Row row = row_of(a, t, a.s.len(t.b), t.first + r);
   const uint64_t part = ((uint64_t)tile * a.n_kv_heads + hk) * a.splits;
@@ -1199,14 +1243,14 @@ __global__ __launch_bounds__(256) void k_attend_tile_join(AttendArgs a) {
 
 // ------------------------------------------------------------------- host
 struct Plan {
-  uint32_t rows;      // 16 or 128 to a workgroup
+  uint32_t rows;      // 16, 128 or 256 to a workgroup
   uint32_t grid;      // workgroups of the 16-row kernel
   uint32_t wg_heads;  // KV heads to one of them
   bool whole, join;   // it cuts no row tile; a second launch is needed
   bool by_unit;       // JoinInfo records: one for each row tile and KV head
   uint64_t infos;
   uint32_t shift;     // log2 of the tokens of a step
-  uint32_t tiles, splits;             // of the 128-row kernel
+  uint32_t tiles, splits;             // of k_attend_tile
   uint64_t part, part_ml, info, total;  // workspace offsets
 };
 
@@ -1221,14 +1265,17 @@ Plan make_plan(const kvc_paged_desc &p, const kvc_paged_batch &b) {
   if (b.n_seqs == 0 || b.n_tokens == 0) return w;
   const uint32_t group = p.n_heads / p.n_kv_heads;
   const uint32_t slots = resident(p.head_dim);
-  // 128-row tiles once the sequences have as many rows to a KV head on average
-  w.rows = b.q_start && (uint64_t)b.n_tokens * group >= (uint64_t)b.n_seqs * 128 ? 128 : 16;
+  // 128-row tiles once the sequences have as many rows to a KV head on average,
+  // 256-row ones (keys and values fetched half as often, but on average half
+  // a tile of each sequence is empty) from eight times as many on
+  const uint64_t avg = b.q_start ? (uint64_t)b.n_tokens * group / b.n_seqs : 0;
+  w.rows = avg < 128 ? 16 : avg < 1024 || p.head_dim == 256 ? 128 : 256;
   // every sequence's last tile may be partly filled
   w.tiles = b.q_start ? (uint32_t)((uint64_t)b.n_tokens * group / w.rows) +
                             std::min(b.n_seqs, b.n_tokens)
                       : b.n_seqs * ((group + 15) / 16);
   w.wg_heads = p.n_kv_heads % 4 == 0 ? 4 : p.n_kv_heads % 2 == 0 ? 2 : 1;
-  if (w.rows == 128) w.wg_heads = 1;
+  if (w.rows != 16) w.wg_heads = 1;
   const uint64_t units = (uint64_t)w.tiles * (p.n_kv_heads / w.wg_heads);
   uint64_t parts = 0;
   if (w.rows == 16) {
@@ -1253,7 +1300,7 @@ Plan make_plan(const kvc_paged_desc &p, const kvc_paged_batch &b) {
     // Equal splits of every row tile: as many as make the workgroups come out
     // in whole rounds, at least 256 tokens to a split.
     const uint64_t most = std::max<uint64_t>(1, ((uint64_t)b.max_len + 255) / 256);
-    w.splits = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(slots / units, most));
+    w.splits = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(slots * 128 / w.rows / units, most));
     w.join = w.splits > 1;
     parts = w.join ? units * w.splits : 0;
   }
@@ -1283,11 +1330,20 @@ hipError_t launch_d(const AttendArgs &a, const Plan &w, hipStream_t stream) {
         hipLaunchKernelGGL((k_attend_rows_join<TI, TC, D, 4>), grid, dim3(256), 0, stream, a);
     }
   } else {
-    hipLaunchKernelGGL((k_attend_tile<TI, TC, D>), dim3(units * w.splits), dim3(256), kBigLds<D>,
-                       stream, a);
-    if (w.join)
-      hipLaunchKernelGGL((k_attend_tile_join<TI, TC, D>), dim3(units * (kBigRows / 4)), dim3(256),
-                         0, stream, a);
+    const auto tile = [&](auto nw) {
+      constexpr int NW = decltype(nw)::value;
+      hipLaunchKernelGGL((k_attend_tile<TI, TC, D, NW>), dim3(units * w.splits), dim3(NW * 64),
+                         (kBigLds<D, NW>), stream, a);
+      if (w.join)
+        hipLaunchKernelGGL((k_attend_tile_join<TI, TC, D, NW * 32>), dim3(units * (NW * 8)),
+                           dim3(256), 0, stream, a);
+    };
+    if constexpr (D != 256)
+      if (w.rows == 256) {
+        tile(std::integral_constant<int, 8>{});
+        return hipGetLastError();
+      }
+    tile(std::integral_constant<int, 4>{});
   }
   return hipGetLastError();
 }

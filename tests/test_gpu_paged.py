@@ -163,6 +163,12 @@ PROMPT = [
     (8, 1, 96, 48, BF16, BF16, [1300], [33], 700),
     (4, 1, 256, 16, F16, F16, [530], [64], 0),
     (6, 2, 64, 7, F16, F16, [64, 128, 127], [64, 64, 127], 65),
+    # 256-row tiles: causal from the first token, a window, a split context, odd pages
+    (16, 1, 64, 16, F16, F16, [130, 200, 77], [130, 64, 77], 0),
+    (32, 2, 128, 20, BF16, BF16, [300], [75], 130),
+    (24, 1, 96, 7, BF16, F16, [1500], [44], 0),
+    (128, 1, 128, 16, F16, F16, [65, 9], [9, 9], 0),
+    (1, 1, 128, 64, BF16, BF16, [1100], [1100], 100),
 ]
 
 
@@ -189,7 +195,7 @@ def test_attend_padding_rows():
     _check_attend(st, out, lse)
 
 
-@pytest.mark.parametrize("heads", [2, 8])
+@pytest.mark.parametrize("heads", [2, 8, 40])  # 16, 128 and 256 rows a workgroup
 @pytest.mark.parametrize("dtype", [F16, BF16])
 def test_attend_nonfinite_hidden_values(dtype, heads):
     """Infinities and NaN in the cached rows of tokens that a row does not
