@@ -808,6 +808,13 @@ _KVC_DTYPE = {torch.float16: 0, torch.bfloat16: 1}
 _DTYPES = (torch.float16, torch.bfloat16)
 
 
+def _u32(x: int, what: str) -> int:
+    """Checks a size that a 32-bit field takes (ctypes would wrap it)."""
+    if not 0 <= x < 1 << 32:
+        raise ValueError(f"{what} must be between 0 and 2^32 - 1")
+    return x
+
+
 def make_paged_desc(n_layers: int, n_heads: int, n_kv_heads: int, head_dim: int, page_tokens: int,
                     n_pages: int, cache_dtype: torch.dtype = torch.float16,
                     io_dtype: Optional[torch.dtype] = None) -> PagedDesc:
@@ -817,8 +824,9 @@ def make_paged_desc(n_layers: int, n_heads: int, n_kv_heads: int, head_dim: int,
     io_dtype = cache_dtype if io_dtype is None else io_dtype
     if cache_dtype not in _KVC_DTYPE or io_dtype not in _KVC_DTYPE:
         raise KvcError(ERR_INVALID_ARG, "make_paged_desc")
-    p = PagedDesc(n_layers, n_heads, n_kv_heads, head_dim, page_tokens, n_pages,
-                  _KVC_DTYPE[cache_dtype], _KVC_DTYPE[io_dtype])
+    sizes = (n_layers, n_heads, n_kv_heads, head_dim, page_tokens, n_pages)
+    p = PagedDesc(*(_u32(x, "a descriptor's size") for x in sizes), _KVC_DTYPE[cache_dtype],
+                  _KVC_DTYPE[io_dtype])
     _check(lib().kvc_validate_paged_desc(ctypes.byref(p)), "make_paged_desc")
     return p
 
@@ -850,7 +858,7 @@ class PagedBatch:
         if any(t is not None and t.device != table.device for t in (lens, q_start)):
             raise ValueError("the batch's tensors must be on one device")
         self.device = table.device
-        self.max_len = max_len
+        self.max_len = None if max_len is None else _u32(max_len, "max_len")
 
     def _args(self, desc: PagedDesc, n_tokens: int) -> _PagedBatch:
         most = self.table.shape[1] * desc.page_tokens
@@ -862,8 +870,9 @@ class PagedBatch:
 
 
 class PagedWorkspace:
-    """Scratch memory and status word of the paged calls for batches of these
-    sizes: n_tokens rows of new tokens (default: one for each sequence)."""
+    """Scratch memory and status word of the paged calls on this batch with
+    n_tokens rows of new tokens (default: one for each sequence).  Calls with
+    other sizes may need more and then raise ERR_CAPACITY."""
 
     def __init__(self, desc: PagedDesc, batch: PagedBatch, n_tokens: Optional[int] = None):
         b = batch._args(desc, batch.n_seqs if n_tokens is None else n_tokens)
@@ -923,7 +932,11 @@ def _paged_stream(stream: Optional[torch.cuda.Stream], device):
     index = device.index
     if index != torch._C._cuda_getDevice():
         raise ValueError("the tensors' device must be the current one")
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device != device:
+        raise ValueError("the stream must belong to the tensors' device")
+    return _stream(stream)
 
 
 def append_async(desc: PagedDesc, batch: PagedBatch, layer: int, pool: torch.Tensor,
@@ -936,6 +949,7 @@ def append_async(desc: PagedDesc, batch: PagedBatch, layer: int, pool: torch.Ten
     dev = batch.device
     n = k.shape[0]
     heads, dim, dtype = desc.n_kv_heads, desc.head_dim, _DTYPES[desc.io_dtype]
+    _u32(layer, "layer")
     ks = _token_rows(k, n, heads, dim, dtype, dev, "k")
     vs = _token_rows(v, n, heads, dim, dtype, dev, "v")
     qs = os_ = 0
@@ -964,8 +978,8 @@ def _attend(name: str, desc: PagedDesc, batch: PagedBatch, layer: int, pool, q, 
     if lse is not None and (lse.shape != (n, heads) or lse.device != dev
                             or lse.dtype != torch.float32 or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous [n_tokens][n_heads] float32 tensor")
-    if window < 0:
-        raise ValueError("window must not be negative")
+    _u32(window, "window")
+    _u32(layer, "layer")
     if wsp.ws.device != dev:
         raise ValueError("the workspace must be on the batch's device")
     _check(getattr(lib(), name)(desc, batch._args(desc, n), layer, _pool_ptr(desc, pool, dev),
@@ -994,8 +1008,10 @@ def attend_prompt_async(desc: PagedDesc, batch: PagedBatch, layer: int, pool: to
     _attend("kvc_attend_prompt", desc, batch, layer, pool, q, out, wsp, scale, window, lse, stream)
 
 
-def _page_args(desc: PagedDesc, pool, table, flat, status):
+def _page_args(desc: PagedDesc, pool, table, flat, status, *tokens):
     dev = pool.device
+    for x in tokens:
+        _u32(x, "a token position or count")
     _int32_tensor(table, 1, "table")
     _int32_tensor(status, 1, "status")
     shape = (desc.n_layers, 2, flat.shape[2], desc.n_kv_heads * desc.head_dim)
@@ -1010,7 +1026,7 @@ def page_out_async(desc: PagedDesc, pool: torch.Tensor, table: torch.Tensor, fir
     """Launch kvc_page_out: tokens [first_token, first_token + n_tokens) of the
     sequence with page ids `table`, every layer, into out [L][2][T][C] from
     token out_first on (no sync; device errors stay in status)."""
-    dev, pp, fp = _page_args(desc, pool, table, out, status)
+    dev, pp, fp = _page_args(desc, pool, table, out, status, first_token, n_tokens, out_first)
     _check(lib().kvc_page_out(desc, pp, table.data_ptr(), table.shape[0], first_token, n_tokens,
                               fp, out.shape[2], out_first, status.data_ptr(),
                               _paged_stream(stream, dev)), "kvc_page_out")
@@ -1021,7 +1037,7 @@ def page_in_async(desc: PagedDesc, kv: torch.Tensor, in_first: int, pool: torch.
                   stream=None) -> None:
     """Launch kvc_page_in: kv [L][2][T][C], tokens from in_first on, into the
     sequence's tokens [first_token, first_token + n_tokens) (no sync)."""
-    dev, pp, fp = _page_args(desc, pool, table, kv, status)
+    dev, pp, fp = _page_args(desc, pool, table, kv, status, first_token, n_tokens, in_first)
     _check(lib().kvc_page_in(desc, fp, kv.shape[2], in_first, pp, table.data_ptr(),
                              table.shape[0], first_token, n_tokens, status.data_ptr(),
                              _paged_stream(stream, dev)), "kvc_page_in")

@@ -252,7 +252,9 @@ __device__ inline uint32_t wave_sums(uint32_t x) {
 template <bool kOne>
 struct Steps {
   uint32_t w[4], upto;  // the lane's sequences; inclusive sum over the lanes
-  __device__ void load(const AttendArgs &a, uint32_t b0, bool check) {
+  // False if the sequences so far have more rows than the batch (q_start
+  // overlaps itself): counting their steps could take without end.
+  __device__ bool load(const AttendArgs &a, uint32_t b0, bool check, uint32_t &rows) {
     const uint32_t lane = threadIdx.x & 63;
     int32_t len[4];
     uint32_t row0[4], n[4];
@@ -268,6 +270,16 @@ struct Steps {
       }
     }
     uint32_t sum = 0;
+    if (!kOne) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum += b0 + lane * 4 + i < a.s.n_seqs ? n[i] : 0;
+      rows += __builtin_amdgcn_readlane(wave_sums(sum), 63);
+      if (rows > a.s.n_tokens) {
+        if (check) set_status(a.status, KVC_ERR_SHAPE);
+        return false;
+      }
+      sum = 0;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       odd = odd || a.s.len_out(len[i]);
@@ -284,6 +296,7 @@ struct Steps {
     }
     if (check && odd) set_status(a.status, KVC_ERR_SHAPE);
     upto = wave_sums(sum);
+    return true;
   }
 };
 
@@ -350,9 +363,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
     if (!by_unit && threadIdx.x == 0 && info) info[blockIdx.x].cut = 0;
     const bool check = blockIdx.x == 0 && wave == 0;
     Steps<kOne> st;
-    uint32_t total = 0;
+    uint32_t total = 0, rows = 0;
     for (uint32_t b0 = 0; b0 < a.s.n_seqs; b0 += 256) {
-      st.load(a, b0, check);
+      if (!st.load(a, b0, check, rows)) return;
       total += __builtin_amdgcn_readlane(st.upto, 63);
     }
     const uint32_t line = total * a.head_groups;
@@ -366,9 +379,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
     hg = at / total;
     uint32_t x = at - hg * total;
     uint32_t base = 0;
+    rows = 0;
     for (uint32_t b0 = 0;; b0 += 256) {  // some sequence holds step x < total
       if (b0 >= a.s.n_seqs) return;
-      if (a.s.n_seqs > 256) st.load(a, b0, false);
+      if (a.s.n_seqs > 256 && !st.load(a, b0, false, rows)) return;
       const uint64_t above = __ballot(base + st.upto > x);
       if (above == 0) {
         base += __builtin_amdgcn_readlane(st.upto, 63);
@@ -858,7 +872,6 @@ __device__ inline bool find_tile(const AttendArgs &a, uint32_t t, Tile &out) {
     const uint32_t b = b0 + lane;
     if (b < a.s.n_seqs) {
       a.s.rows(b, row0, n);
-      if (t == 0 && a.s.rows_bad(b)) set_status(a.status, KVC_ERR_SHAPE);
     }
     const uint32_t mine = (n * a.group + kRows - 1) / kRows;
     uint32_t sum = mine;
@@ -904,9 +917,9 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tile(
   const uint32_t rest = blockIdx.x / a.n_kv_heads;
   const uint32_t split = rest % a.splits, tile = rest / a.splits;
   Tile t;
+  if (blockIdx.x == 0) a.s.check(a.status);
   if (!find_tile<kRows>(a, tile, t)) return;
   const int32_t len = a.s.len(t.b);
-  if (threadIdx.x == 0 && a.s.len_bad(t.b)) set_status(a.status, KVC_ERR_SHAPE);
   const uint32_t w0 = wave * 32;
   const bool busy = w0 < t.rows;  // the wave has rows
   const bool live = w0 + n32 < t.rows;
@@ -1265,11 +1278,19 @@ Plan make_plan(const kvc_paged_desc &p, const kvc_paged_batch &b) {
   if (b.n_seqs == 0 || b.n_tokens == 0) return w;
   const uint32_t group = p.n_heads / p.n_kv_heads;
   const uint32_t slots = resident(p.head_dim);
-  // 128-row tiles once the sequences have as many rows to a KV head on average,
-  // 256-row ones (keys and values fetched half as often, but on average half
-  // a tile of each sequence is empty) from eight times as many on
+  // The 16-row kernel reads a sequence's cache once for every 16 rows, so it
+  // is for sequences of a few rows to a KV head.  If they have 128 on average,
+  // or if there may be one with 1,024 among them (all tokens but one each), the
+  // tile kernel is taken, which gives a short one a mostly empty tile but
+  // still reads as fast as HBM; with 256-row tiles (keys and values fetched
+  // half as often, on average half a tile of a sequence empty) from 1,024 rows
+  // a sequence on.
   const uint64_t avg = b.q_start ? (uint64_t)b.n_tokens * group / b.n_seqs : 0;
-  w.rows = avg < 128 ? 16 : avg < 1024 || p.head_dim == 256 ? 128 : 256;
+  const uint64_t longest =
+      b.q_start && b.n_tokens > b.n_seqs ? (uint64_t)(b.n_tokens - b.n_seqs) * group : 0;
+  w.rows = avg < 128 && longest < 1024           ? 16
+           : avg < 1024 || p.head_dim == 256 ? 128
+                                                 : 256;
   // every sequence's last tile may be partly filled
   w.tiles = b.q_start ? (uint32_t)((uint64_t)b.n_tokens * group / w.rows) +
                             std::min(b.n_seqs, b.n_tokens)

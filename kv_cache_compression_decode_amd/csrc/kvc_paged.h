@@ -109,6 +109,13 @@ struct Seqs {
   }
   __host__ __device__ inline int32_t len(uint32_t b) const { return clamp_len(lens[b]); }
   __host__ __device__ inline bool len_bad(uint32_t b) const { return len_out(lens[b]); }
+  // A workgroup reports what is wrong with any sequence's rows or length.
+  __device__ inline void check(int32_t *status) const {
+    bool bad = false;
+    for (uint32_t b = threadIdx.x; b < n_seqs; b += blockDim.x)
+      bad = bad || rows_bad(b) || len_bad(b);
+    if (bad) set_status(status, KVC_ERR_SHAPE);
+  }
   // Slot (token row of the pool) of token `in` of page `id`.  False for an id
   // outside the pool; the slot is then one inside it, so that a caller that
   // goes on reads nothing out of bounds.

@@ -161,10 +161,8 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
   uint32_t r0, n;
   a.s.rows(b, r0, n);
   const bool first = threadIdx.x == 0 && blockIdx.y == 0;
-  if (a.s.rows_bad(b) || a.s.len_bad(b)) {
-    if (first) set_status(a.status, KVC_ERR_SHAPE);
-    return;
-  }
+  if (blockIdx.x == 0 && blockIdx.y == 0) a.s.check(a.status);
+  if (a.s.rows_bad(b) || a.s.len_bad(b)) return;
   if (row < r0 || row - r0 >= n) return;  // before the first or behind the last sequence
   const int32_t pos = a.s.lens[b] - (int32_t)n + (int32_t)(row - r0);
   if (pos < 0) return;  // padding

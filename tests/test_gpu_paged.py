@@ -163,6 +163,9 @@ PROMPT = [
     (8, 1, 96, 48, BF16, BF16, [1300], [33], 700),
     (4, 1, 256, 16, F16, F16, [530], [64], 0),
     (6, 2, 64, 7, F16, F16, [64, 128, 127], [64, 64, 127], 65),
+    # a long prompt beside single tokens, and many of a few tokens
+    (8, 1, 64, 16, F16, F16, [300] + [70 + 9 * i for i in range(40)], [140] + [1] * 40, 0),
+    (8, 2, 64, 16, BF16, F16, [50 + 11 * i for i in range(70)], [4] * 70, 0),
     # 256-row tiles: causal from the first token, a window, a split context, odd pages
     (16, 1, 64, 16, F16, F16, [130, 200, 77], [130, 64, 77], 0),
     (32, 2, 128, 20, BF16, BF16, [300], [75], 130),
@@ -450,6 +453,65 @@ def test_device_errors_are_reported():
         assert code(st) == kvc.ERR_SHAPE
         kvc.append_async(st.desc, st.batch, 1, st.pool, st.k, st.v, st.wsp)
         assert code(st) == kvc.ERR_SHAPE
+
+
+@pytest.mark.parametrize("heads", [2, 64])  # 16 rows a workgroup, and tiles
+def test_q_start_that_overlaps_itself(heads):
+    """Every other sequence claims all rows: reported, and the call ends."""
+    n = 600
+    st = Setup([40] * n, [1] * n, heads, 1, 64, 16, F16, F16)
+    st.batch.q_start[0::2] = 0
+    st.batch.q_start[1::2] = n
+    out = torch.zeros((n, heads, 64), dtype=F16, device=DEV)
+    kvc.attend_prompt_async(st.desc, st.batch, 1, st.pool, st.q, out, st.wsp)
+    assert int(st.wsp.status.item()) == kvc.ERR_SHAPE
+    st.wsp.status.zero_()
+    kvc.append_async(st.desc, st.batch, 1, st.pool, st.k, st.v, st.wsp)
+    assert int(st.wsp.status.item()) == kvc.ERR_SHAPE
+
+
+def test_binding_refuses_what_it_cannot_pass_on():
+    st = Setup([40], [1], 4, 2, 64, 16, F16, F16, single=True)
+    out = torch.empty_like(st.q.contiguous())
+    flat = torch.zeros((2, 2, 50, 128), dtype=F16, device=DEV)
+
+    def attend(**kw):
+        a = dict(layer=1, pool=st.pool, q=st.q, out=out, window=0, lse=None)
+        a.update(kw)
+        kvc.attend_async(st.desc, st.batch, a["layer"], a["pool"], a["q"], a["out"], st.wsp,
+                         window=a["window"], lse=a["lse"])
+
+    for bad in (dict(layer=-1), dict(layer=1 << 32), dict(window=-1), dict(window=1 << 32),
+                dict(pool=st.pool[:1]), dict(pool=st.pool.to(BF16)), dict(q=st.q.to(BF16)),
+                dict(q=st.q.cpu()), dict(q=st.q.transpose(1, 2)), dict(out=out[:, :2]),
+                dict(lse=torch.zeros((1, 3), device=DEV)),
+                dict(lse=torch.zeros((1, 4), dtype=torch.float64, device=DEV))):
+        with pytest.raises(ValueError):
+            attend(**bad)
+    with pytest.raises(kvc.KvcError):
+        attend(layer=2)
+    for first, n, at in ((1 << 32, 1, 0), (0, -1, 0), (0, 1, 1 << 32)):
+        with pytest.raises(ValueError):
+            kvc.page_out_async(st.desc, st.pool, st.table[0], first, n, flat, at, st.wsp.status)
+    with pytest.raises(ValueError):
+        kvc.PagedBatch(st.table, st.lens, max_len=1 << 32)
+    with pytest.raises(ValueError):
+        kvc.PagedBatch(st.table, st.lens.to(torch.int64))
+    with pytest.raises(ValueError):
+        kvc.make_paged_desc(1, 8, 2, 64 + (1 << 32), 16, 4)
+    small = kvc.PagedWorkspace(st.desc, st.batch)
+    long = kvc.PagedBatch(torch.zeros((1, 4), dtype=torch.int32, device=DEV), st.lens, max_len=64)
+    attend()  # and a good call still goes through
+    assert int(st.wsp.status.item()) == 0
+    big = kvc.make_paged_desc(2, 4, 2, 64, 1 << 20, 4)
+    pool = torch.zeros((1,), dtype=F16, device=DEV)
+    with pytest.raises(ValueError):
+        kvc.attend_async(big, long, 1, pool, st.q, out, small)
+    table = torch.zeros((1, 400), dtype=torch.int32, device=DEV)
+    wide = kvc.PagedBatch(table, st.lens)
+    with pytest.raises(kvc.KvcError) as e:  # a longer cache needs more scratch
+        kvc.attend_async(st.desc, wide, 1, st.pool, st.q, out, small)
+    assert e.value.code == kvc.ERR_CAPACITY
 
 
 def test_status_word_is_sticky():
