@@ -141,29 +141,6 @@ __device__ inline bool nonfinite2(uint32_t w) {
   return (w & e) == e || (w & (e << 16)) == (e << 16);
 }
 
-// ------------------------------------------------------------ row tiles
-// Rows [first, first + rows) of sequence b.
-struct Tile {
-  uint32_t b, row0, n;  // the sequence, its first token row and token count
-  uint32_t first, rows;
-};
-
-// Where a row writes, and its visible tokens [lo, hi).
-struct Row {
-  uint32_t token, head;  // row of q and out; head within the group
-  int32_t lo, hi;
-};
-__device__ inline Row row_of(const AttendArgs &a, const Tile &t, int32_t len, uint32_t r) {
-  Row w;
-  const uint32_t i = a.group_div.div(r);
-  w.head = r - i * a.group;
-  w.token = t.row0 + i;
-  const int32_t pos = len - (int32_t)t.n + (int32_t)i;
-  w.hi = pos < 0 ? 0 : pos + 1;
-  w.lo = a.window != 0 && (uint32_t)w.hi > a.window ? w.hi - (int32_t)a.window : 0;
-  return w;
-}
-
 // ---------------------------------------------------- sharing out the tokens
 // The work of a call is a line of steps (a tile of 32 tokens for one row tile
 // and KV head; more tiles where a call's steps would pass 31 bits): head by head, in each the row tiles in sequence order,
@@ -188,50 +165,34 @@ constexpr uint32_t resident(uint32_t head_dim) { return (head_dim == 256 ? 1 : 2
 constexpr uint32_t kRowTile = 16;
 constexpr uint32_t kTok = 32;
 
-// kOne: one new token a sequence (q_start is NULL).
-template <bool kOne>
 struct Work {
-  uint32_t b, k;            // the sequence and its row tile
-  uint32_t row0, n, tiles;  // its token rows and row tiles
+  uint32_t b, k;  // the sequence and its row tile
   int32_t len;
 
-  // steps of row tile k of a sequence: at least one, so that every row is written
-  __device__ static uint32_t steps_of(const AttendArgs &a, uint32_t n, int32_t len, uint32_t k) {
+  // steps of a row tile of a sequence: at least one, so that every row is written
+  __device__ static uint32_t steps_of(const AttendArgs &a, int32_t len) {
     if (a.whole) return 1;
-    int32_t h0 = len, hi = len;  // one past the first and the last row's position
-    if (!kOne) {
-      const uint32_t first = k * kRowTile, last = min(first + kRowTile, n * a.group) - 1;
-      const int32_t base = len - (int32_t)n + 1;
-      h0 = max(base + (int32_t)a.group_div.div(first), 0);
-      hi = max(base + (int32_t)a.group_div.div(last), 0);
-    }
-    const int32_t lo = a.window != 0 && (uint32_t)h0 > a.window ? h0 - (int32_t)a.window : 0;
-    return (hi > lo ? ((uint32_t)(hi - lo) - 1) >> a.step_shift : 0) + 1;
+    const int32_t n = len - first_of(a, len);
+    return (n > 0 ? ((uint32_t)n - 1) >> a.step_shift : 0) + 1;
   }
-  __device__ static uint32_t tiles_of(const AttendArgs &a, uint32_t n) {
-    return (n * a.group + kRowTile - 1) / kRowTile;
+  // the first visible token
+  __device__ static int32_t first_of(const AttendArgs &a, int32_t len) {
+    return a.window != 0 && (uint32_t)len > a.window ? len - (int32_t)a.window : 0;
   }
   __device__ void load(const AttendArgs &a, uint32_t seq) {
     b = seq;
-    row0 = seq;
-    n = 1;
-    if (!kOne) a.s.rows(b, row0, n);
-    tiles = tiles_of(a, n);
     len = a.s.len(b);
   }
-  __device__ uint32_t steps(const AttendArgs &a) const { return steps_of(a, n, len, k); }
   // the next row tile; after the last sequence's, the first one's (next head)
   __device__ void next(const AttendArgs &a, uint32_t &head) {
-    if (++k < tiles) return;
+    if (++k < a.seq_tiles) return;
     k = 0;
-    uint32_t s = b;
-    do {
-      if (++s == a.s.n_seqs) {
-        s = 0;
-        ++head;
-      }
-      load(a, s);
-    } while (!kOne && tiles == 0);
+    uint32_t s = b + 1;
+    if (s == a.s.n_seqs) {
+      s = 0;
+      ++head;
+    }
+    load(a, s);
   }
 };
 
@@ -249,54 +210,25 @@ __device__ inline uint32_t wave_sums(uint32_t x) {
 
 // 256 sequences' steps at a time, four to a lane (their loads in flight
 // together).
-template <bool kOne>
 struct Steps {
   uint32_t w[4], upto;  // the lane's sequences; inclusive sum over the lanes
-  // False if the sequences so far have more rows than the batch (q_start
-  // overlaps itself): counting their steps could take without end.
-  __device__ bool load(const AttendArgs &a, uint32_t b0, bool check, uint32_t &rows) {
+  __device__ void load(const AttendArgs &a, uint32_t b0, bool check) {
     const uint32_t lane = threadIdx.x & 63;
     int32_t len[4];
-    uint32_t row0[4], n[4];
-    bool odd = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t b = min(b0 + lane * 4 + i, a.s.n_seqs - 1);
-      len[i] = a.s.lens[b];
-      n[i] = 1;
-      if (!kOne) {
-        a.s.rows(b, row0[i], n[i]);
-        odd = odd || a.s.rows_bad(b);
-      }
-    }
+    for (int i = 0; i < 4; ++i) len[i] = a.s.lens[min(b0 + lane * 4 + i, a.s.n_seqs - 1)];
     uint32_t sum = 0;
-    if (!kOne) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sum += b0 + lane * 4 + i < a.s.n_seqs ? n[i] : 0;
-      rows += __builtin_amdgcn_readlane(wave_sums(sum), 63);
-      if (rows > a.s.n_tokens) {
-        if (check) set_status(a.status, KVC_ERR_SHAPE);
-        return false;
-      }
-      sum = 0;
-    }
+    bool bad = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      odd = odd || a.s.len_out(len[i]);
-      const int32_t m = a.s.clamp_len(len[i]);
-      const uint32_t tiles = Work<kOne>::tiles_of(a, n[i]);
-      uint32_t steps = 0;
-      if (kOne || a.whole) {
-        steps = tiles * (a.whole ? 1 : Work<kOne>::steps_of(a, 1, m, 0));
-      } else {
-        for (uint32_t k = 0; k < tiles; ++k) steps += Work<kOne>::steps_of(a, n[i], m, k);
-      }
-      w[i] = b0 + lane * 4 + i < a.s.n_seqs ? steps : 0;
+      bad = bad || a.s.len_out(len[i]);
+      w[i] = b0 + lane * 4 + i < a.s.n_seqs
+                 ? a.seq_tiles * Work::steps_of(a, a.s.clamp_len(len[i]))
+                 : 0;
       sum += w[i];
     }
-    if (check && odd) set_status(a.status, KVC_ERR_SHAPE);
+    if (check && bad) set_status(a.status, KVC_ERR_SHAPE);
     upto = wave_sums(sum);
-    return true;
   }
 };
 
@@ -314,15 +246,20 @@ struct Pieces {
 // What the workgroup that holds a row tile's first part leaves for the join:
 // whether there are others, and which workgroups hold them.  One for each
 // workgroup (whose last part alone can be cut and the first of its row tile),
-// or, where single tokens have fewer row tiles than that, one for each row
-// tile and KV head (`by_unit`), so that the join launches no idle workgroups.
+// or, where there are fewer row tiles than that, one for each row tile and
+// head (`by_unit`), so that the join launches no idle workgroups.
 struct JoinInfo {
   uint32_t cut, b, k, head, first, last, slot, pad;
 };
 
-// ------------------------------------------------------- 16 rows a workgroup
-// The four waves of a workgroup share 16 rows and take tiles of 32 tokens in
-// turn; they are joined through LDS at the end.
+// ------------------------------------------------- one new token a sequence
+// A row tile is up to 16 of the query heads that share a KV head; all see the
+// same tokens.  The waves of a head take tiles of 32 tokens in turn.
+//
+// What bounds it is HBM: 4 head_dim bytes a token and head, against which a
+// wave has some 150 vector instructions and 16 products for 32 tokens (a
+// tenth of the time).  20 sequences of 32 heads x 128 (1.33 GB): 215 us, 6.2
+// TB/s (a bare read of the same pages in the same order: 6.4).
 //
 // Scores are computed transposed, S^T = K Q^T: lane l holds row l%16's scores
 // of tokens (l/16)*4 .. +3 of both halves of the tile.  That is the layout in
@@ -333,7 +270,7 @@ struct JoinInfo {
 // dimensions of its eight tokens (16 lanes cover whole rows, so the loads are
 // contiguous) and the i-th product takes dimension l%16 * E + i, a byte
 // permutation in registers.  Neither K nor V passes through LDS.
-template <class TI, class TC, int D, bool kOne>
+template <class TI, class TC, int D>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArgs a) {
   constexpr int E = D / 16;
   constexpr int KK = D / 32;
@@ -344,33 +281,31 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
   const uint32_t n16 = lane & 15, g4 = lane >> 4;
 
   // this workgroup's piece of the line, and where it begins
-  Work<kOne> u;
+  Work u;
   uint32_t hg;
   uint32_t at, stop, off;  // off: steps of the first row tile before the piece
   Pieces pc{gridDim.x, 1, 0};
   JoinInfo *info = static_cast<JoinInfo *>(a.info);
-  const uint32_t per = Work<kOne>::tiles_of(a, 1);  // row tiles of a single token
-  if (kOne && a.whole) {  // a row tile to a workgroup: no search
+  if (a.whole) {  // a row tile to a workgroup: no search
     const uint32_t unit = blockIdx.x / a.head_groups;
     hg = blockIdx.x - unit * a.head_groups;
-    u.load(a, unit / per);
-    u.k = unit - u.b * per;
+    u.load(a, unit / a.seq_tiles);
+    u.k = unit - u.b * a.seq_tiles;
     at = off = 0;
     stop = 1;
     if (threadIdx.x == 0 && a.s.len_bad(u.b)) set_status(a.status, KVC_ERR_SHAPE);
   } else {
-    const bool by_unit = kOne && a.by_unit;
-    if (!by_unit && threadIdx.x == 0 && info) info[blockIdx.x].cut = 0;
+    if (!a.by_unit && threadIdx.x == 0) info[blockIdx.x].cut = 0;
     const bool check = blockIdx.x == 0 && wave == 0;
-    Steps<kOne> st;
-    uint32_t total = 0, rows = 0;
+    Steps st;
+    uint32_t total = 0;
     for (uint32_t b0 = 0; b0 < a.s.n_seqs; b0 += 256) {
-      if (!st.load(a, b0, check, rows)) return;
+      st.load(a, b0, check);
       total += __builtin_amdgcn_readlane(st.upto, 63);
     }
     const uint32_t line = total * a.head_groups;
     // at least min_steps to a workgroup
-    pc.parts = min(gridDim.x, a.whole ? line : (line + a.min_steps - 1) / a.min_steps);
+    pc.parts = min(gridDim.x, (line + a.min_steps - 1) / a.min_steps);
     if (blockIdx.x >= pc.parts) return;
     pc.per = line / pc.parts;
     pc.rem = line - pc.per * pc.parts;
@@ -379,10 +314,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
     hg = at / total;
     uint32_t x = at - hg * total;
     uint32_t base = 0;
-    rows = 0;
     for (uint32_t b0 = 0;; b0 += 256) {  // some sequence holds step x < total
       if (b0 >= a.s.n_seqs) return;
-      if (a.s.n_seqs > 256 && !st.load(a, b0, false, rows)) return;
+      if (a.s.n_seqs > 256) st.load(a, b0, false);
       const uint64_t above = __ballot(base + st.upto > x);
       if (above == 0) {
         base += __builtin_amdgcn_readlane(st.upto, 63);
@@ -404,17 +338,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
           ++b;
         }
       u.load(a, b);
-      u.k = 0;
-      if (kOne) {
-        const uint32_t s = u.steps(a);
-        u.k = min(x / s, u.tiles - 1);
-        x -= u.k * s;
-      } else {
-        for (uint32_t s = u.steps(a); x >= s && u.k + 1 < u.tiles; s = u.steps(a)) {
-          x -= s;
-          ++u.k;
-        }
-      }
+      const uint32_t steps = Work::steps_of(a, u.len);
+      u.k = min(x / steps, a.seq_tiles - 1);
+      x -= u.k * steps;
       break;
     }
     off = x;
@@ -429,26 +355,23 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
   while (at < stop && hg < a.head_groups) {
     const uint32_t hk = hg * a.wg_heads + my_head;
     // the part of row tile u.k that this workgroup holds: steps [s_lo, s_hi)
-    const uint32_t steps = u.steps(a);
+    const uint32_t steps = Work::steps_of(a, u.len);
     const uint32_t left = min(steps - off, stop - at);
-    const Tile t{u.b, u.row0, u.n, u.k * kRowTile, min(kRowTile, u.n * a.group - u.k * kRowTile)};
-    const bool live = n16 < t.rows;
-    const Row row = row_of(a, t, u.len, t.first + (live ? n16 : 0));
-    const Row r_first = row_of(a, t, u.len, t.first);
-    const Row r_last = row_of(a, t, u.len, t.first + t.rows - 1);
-    const int32_t begin = r_first.lo, end = r_last.hi;  // lo and hi grow with the row
+    const uint32_t first = u.k * kRowTile, rows = min(kRowTile, a.group - first);
+    const bool live = n16 < rows;
+    const int32_t begin = Work::first_of(a, u.len), end = u.len;
     const int32_t tiles = end > begin ? (int32_t)(((uint32_t)(end - begin) + kTok - 1) / kTok) : 0;
     // a step is 2^(step_shift - 5) tiles
     const uint32_t per_step = a.step_shift - 5;
     const int32_t t_lo = a.whole ? 0 : (int32_t)(off << per_step);
     const int32_t t_hi = a.whole ? tiles : min(tiles, (int32_t)((off + left) << per_step));
-    const uint32_t qh = hk * a.group + row.head;
+    const uint32_t qh = hk * a.group + first + (live ? n16 : 0);
 
     float m = ninf(), l = 0.0f;
     f32x4 o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = f32x4{0, 0, 0, 0};
-    const int32_t *table = a.s.table + (uint64_t)t.b * a.s.table_stride;
+    const int32_t *table = a.s.table + (uint64_t)u.b * a.s.table_stride;
     const TC *kbase = kcache + (uint64_t)hk * D, *vbase = vcache + (uint64_t)hk * D;
     const int32_t last = end - 1;
     // Each lane looks up one token of a tile (the others' slots come by
@@ -466,12 +389,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) qf[kk] = u32x4{0, 0, 0, 0};
     if (live) {
-      const TI *q = static_cast<const TI *>(a.q) + (uint64_t)row.token * a.q_stride +
+      const TI *q = static_cast<const TI *>(a.q) + (uint64_t)u.b * a.q_stride +
                     (uint64_t)qh * D + g4 * 8;
 #pragma unroll
       for (int kk = 0; kk < KK; ++kk) qf[kk] = load_q8<TI, TC>(q + kk * 32, sc_q);
     }
-
 
     for (int32_t ti = t_lo + (int32_t)turn; ti < t_hi; ti += (int32_t)turns) {
       const int32_t j0 = begin + ti * (int32_t)kTok;
@@ -506,14 +428,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
       float x[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = sc[i >> 2][i & 3] * sc_q.s;
-      // some token of the tile is hidden from some row
-      const bool edge = j0 < r_last.lo || j0 + (int32_t)kTok > r_first.hi;
+      const bool edge = j0 + (int32_t)kTok > end;  // some tokens are hidden
       if (edge) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int32_t j = j0 + (i >> 2) * 16 + (int32_t)g4 * 4 + (i & 3);
-          x[i] = j >= row.lo && j < row.hi ? x[i] : ninf();
-        }
+        for (int i = 0; i < 8; ++i)
+          x[i] = j0 + (i >> 2) * 16 + (int32_t)g4 * 4 + (i & 3) < end ? x[i] : ninf();
       }
       float mt = x[0];
 #pragma unroll
@@ -540,51 +459,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
 
       if (edge) {
         // A hidden token's probability is 0, but 0 times an infinity or NaN of
-        // its value row is not: tokens hidden from every row are zeroed here,
-        // and a token that some rows see and others do not (its row of V not
-        // finite) is taken out of the product and added lane by lane, where
-        // the row's own visibility decides.
-        bool odd = false;
+        // its value row would not be.
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int32_t j = j0 + (i >> 2) * 16 + (int32_t)g4 * 4 + (i & 3);
-          bool nf = false;
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-          for (int w = 0; w < E / 2; ++w) {
-            if (j >= end || j < begin) vf[i].w[w] = 0;
-            nf = nf || nonfinite2<TC>(vf[i].w[w]);
-          }
-          odd = odd || nf;
-        }
-        if (__ballot(odd)) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            bool nf = false;
-#pragma unroll
-            for (int w = 0; w < E / 2; ++w) nf = nf || nonfinite2<TC>(vf[i].w[w]);
-            const uint64_t who = __ballot(nf);
-            for (uint32_t g = 0; g < 4; ++g) {
-              if (((who >> (16 * g)) & 0xFFFFu) == 0) continue;
-              // token (half, g, i): its probability for this lane's row is in
-              // lane g*16 + n16; its values at this lane's output dimensions
-              const int32_t j = j0 + (i >> 2) * 16 + (int32_t)g * 4 + (i & 3);
-              const float pj = __shfl(p[i], (int)(g * 16 + n16));
-              const uint32_t sj = __shfl(vslot[i], (int)(g * 16));
-              if (g4 == g) {
-#pragma unroll
-                for (int w = 0; w < E / 2; ++w) vf[i].w[w] = 0;
-              }
-              if (j >= row.lo && j < row.hi) {
-                const TC *vp = vbase + (uint64_t)sj * a.row;
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-#pragma unroll
-                  for (int c = 0; c < 4; ++c)
-                    o[e][c] = __builtin_fmaf(pj, (float)vp[(g4 * 4 + c) * E + e], o[e][c]);
-              }
-            }
-          }
-        }
+          for (int w = 0; w < E / 2; ++w)
+            if (j0 + (i >> 2) * 16 + (int32_t)g4 * 4 + (i & 3) >= end) vf[i].w[w] = 0;
       }
 #pragma unroll
       for (int e = 0; e < E; ++e) {
@@ -599,7 +479,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
 
-    const bool some = row.hi > row.lo;
+    const bool some = end > begin;
     const bool single = off == 0 && left == steps;
     const uint32_t slot = at == piece ? 0 : 1;
     const uint64_t part = ((uint64_t)blockIdx.x * 2 + slot) * a.wg_heads + my_head;
@@ -620,16 +500,16 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
     }
     const float f = __builtin_amdgcn_exp2f(m - (mm == ninf() ? 0.0f : mm)) *
                     (single ? (some ? 1.0f / ll : 0.0f) : 1.0f);
-    if (turn == 0 && lane < t.rows) {
+    if (turn == 0 && lane < rows) {
       if (!single) {
         a.part_ml[part * 32 + lane] = mm;
         a.part_ml[part * 32 + 16 + lane] = ll;
       } else if (a.lse) {
-        a.lse[(uint64_t)row.token * a.n_heads + qh] =
+        a.lse[(uint64_t)u.b * a.n_heads + qh] =
             some ? (mm - kShift<TC> + __builtin_amdgcn_logf(ll)) * kLn2 : ninf();
       }
     }
-    TI *out = static_cast<TI *>(a.out) + (uint64_t)row.token * a.out_stride + (uint64_t)qh * D;
+    TI *out = static_cast<TI *>(a.out) + (uint64_t)u.b * a.out_stride + (uint64_t)qh * D;
     float *part_o = a.part + (part * 16 + n16) * D;
     if (turns == 1) {
       // a lane's 4E values are dimensions g4 * 4E on of its row
@@ -667,7 +547,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
         __syncthreads();
         // the head's waves add up 16 rows of 16 * EC dimensions, two dimensions
         // at a time; x of them stands for dimension x / EC * E + e0 + x % EC
-        for (uint32_t i = turn * 64 + lane; i < t.rows * 8u * EC; i += turns * 64) {
+        for (uint32_t i = turn * 64 + lane; i < rows * 8u * EC; i += turns * 64) {
           const uint32_t r = i / (8u * EC), x = (i - r * (8u * EC)) * 2;
           float v0 = 0.0f, v1 = 0.0f;
           for (uint32_t w = 0; w < turns; ++w) {
@@ -676,11 +556,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
           }
           const uint32_t dim = E == EC ? x : (x / EC) * E + e0 + x % EC;
           if (single) {
-            const Row w = row_of(a, t, u.len, t.first + r);
             uint32_t *op = reinterpret_cast<uint32_t *>(
-                static_cast<TI *>(a.out) + (uint64_t)w.token * a.out_stride +
-                (uint64_t)(hk * a.group + w.head) * D + dim);
-            *op = w.hi > w.lo ? pack2<TI>(v0, v1) : 0u;
+                static_cast<TI *>(a.out) + (uint64_t)u.b * a.out_stride +
+                (uint64_t)(hk * a.group + first + r) * D + dim);
+            *op = some ? pack2<TI>(v0, v1) : 0u;
           } else {
             float *op = a.part + (part * 16 + r) * D + dim;
             op[0] = v0;
@@ -691,11 +570,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
     }
     if (threadIdx.x == 0 && off == 0 && info) {
       const bool cut = left < steps;
-      const bool by_unit = kOne && a.by_unit;
-      const uint32_t id = by_unit ? (u.b * per + u.k) * a.head_groups + hg : blockIdx.x;
+      const uint32_t id =
+          a.by_unit ? (u.b * a.seq_tiles + u.k) * a.head_groups + hg : blockIdx.x;
       if (cut)
         info[id] = JoinInfo{1, u.b, u.k, hg, blockIdx.x, pc.owner(at + steps - 1), slot, 0};
-      else if (by_unit)
+      else if (a.by_unit)
         info[id].cut = 0;
     }
     at += left;
@@ -722,11 +601,7 @@ __global__ __launch_bounds__(W * 64) void k_attend_rows_join(AttendArgs a) {
   if (info.cut != 1 || info.b >= a.s.n_seqs || info.first > info.last || info.last >= a.pieces)
     return;
   const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = blockIdx.y;
-  uint32_t row0, n;
-  a.s.rows(info.b, row0, n);
-  if (info.k * kRowTile >= n * a.group) return;
-  const Tile t{info.b, row0, n, info.k * kRowTile, min(kRowTile, n * a.group - info.k * kRowTile)};
-  if (r >= t.rows) return;
+  if (info.k * kRowTile + r >= a.group || info.head >= a.head_groups) return;
   const uint32_t parts = info.last - info.first + 1;
   auto part_of = [&](uint32_t i) {
     return ((uint64_t)(info.first + i) * 2 + (i == 0 ? info.slot : 0)) * a.wg_heads + blockIdx.z;
@@ -793,11 +668,10 @@ __global__ __launch_bounds__(W * 64) void k_attend_rows_join(AttendArgs a) {
   l = 0.0f;
 #pragma unroll
   for (uint32_t w = 0; w < W; ++w) l += s_l[w];
-  const Row row = row_of(a, t, len, t.first + r);
-  const bool some = row.hi > row.lo;
+  const bool some = len > 0;
   const float inv = some ? 1.0f / l : 0.0f;
-  const uint32_t h = (info.head * a.wg_heads + blockIdx.z) * a.group + row.head;
-  TI *out = static_cast<TI *>(a.out) + (uint64_t)row.token * a.out_stride + (uint64_t)h * D;
+  const uint32_t h = (info.head * a.wg_heads + blockIdx.z) * a.group + info.k * kRowTile + r;
+  TI *out = static_cast<TI *>(a.out) + (uint64_t)info.b * a.out_stride + (uint64_t)h * D;
   if (threadIdx.x < D / 2) {
     const uint32_t x = threadIdx.x * 2;
     float v0 = 0.0f, v1 = 0.0f;
@@ -809,7 +683,7 @@ __global__ __launch_bounds__(W * 64) void k_attend_rows_join(AttendArgs a) {
     *reinterpret_cast<uint32_t *>(out + x) = some ? pack2<TI>(v0 * inv, v1 * inv) : 0u;
   }
   if (threadIdx.x == 0 && a.lse)
-    a.lse[(uint64_t)row.token * a.n_heads + h] =
+    a.lse[(uint64_t)info.b * a.n_heads + h] =
         some ? (mm - kShift<TC> + __builtin_amdgcn_logf(l)) * kLn2 : ninf();
 }
 
@@ -857,6 +731,28 @@ constexpr int val_bufs(int waves) { return waves == 8 ? 3 : 2; }
 template <int D, int NW>
 constexpr uint32_t kBigLds = 2 * kKeyBuf<D> + val_bufs(NW) * kValBuf<D> + 32;
 __device__ inline uint32_t next_odd_of(uint32_t i) { return i == 2 ? 0 : i + 1; }
+
+// Rows [first, first + rows) of sequence b.
+struct Tile {
+  uint32_t b, row0, n;  // the sequence, its first token row and token count
+  uint32_t first, rows;
+};
+
+// Where a row writes, and its visible tokens [lo, hi).
+struct Row {
+  uint32_t token, head;  // row of q and out; head within the group
+  int32_t lo, hi;
+};
+__device__ inline Row row_of(const AttendArgs &a, const Tile &t, int32_t len, uint32_t r) {
+  Row w;
+  const uint32_t i = a.group_div.div(r);
+  w.head = r - i * a.group;
+  w.token = t.row0 + i;
+  const int32_t pos = len - (int32_t)t.n + (int32_t)i;
+  w.hi = pos < 0 ? 0 : pos + 1;
+  w.lo = a.window != 0 && (uint32_t)w.hi > a.window ? w.hi - (int32_t)a.window : 0;
+  return w;
+}
 
 // Row tile `t` of the call: the sequences in order, of each its last tile (the
 // one with the most visible tokens) first, so that a launch ends with short
@@ -1278,19 +1174,13 @@ Plan make_plan(const kvc_paged_desc &p, const kvc_paged_batch &b) {
   if (b.n_seqs == 0 || b.n_tokens == 0) return w;
   const uint32_t group = p.n_heads / p.n_kv_heads;
   const uint32_t slots = resident(p.head_dim);
-  // The 16-row kernel reads a sequence's cache once for every 16 rows, so it
-  // is for sequences of a few rows to a KV head.  If they have 128 on average,
-  // or if there may be one with 1,024 among them (all tokens but one each), the
-  // tile kernel is taken, which gives a short one a mostly empty tile but
-  // still reads as fast as HBM; with 256-row tiles (keys and values fetched
-  // half as often, on average half a tile of a sequence empty) from 1,024 rows
-  // a sequence on.
+  // Several tokens go to the tile kernel however few they are (8 sequences of
+  // 4 tokens and 8 heads to a KV head, 8,000 in the cache: 67 us against 99
+  // for 16-row tiles, which read a cache once for every 16 rows); with 256-row
+  // tiles (keys and values fetched half as often, on average half a tile of a
+  // sequence empty) from 1,024 rows a sequence on.
   const uint64_t avg = b.q_start ? (uint64_t)b.n_tokens * group / b.n_seqs : 0;
-  const uint64_t longest =
-      b.q_start && b.n_tokens > b.n_seqs ? (uint64_t)(b.n_tokens - b.n_seqs) * group : 0;
-  w.rows = avg < 128 && longest < 1024           ? 16
-           : avg < 1024 || p.head_dim == 256 ? 128
-                                                 : 256;
+  w.rows = !b.q_start ? 16 : avg < 1024 || p.head_dim == 256 ? 128 : 256;
   // every sequence's last tile may be partly filled
   w.tiles = b.q_start ? (uint32_t)((uint64_t)b.n_tokens * group / w.rows) +
                             std::min(b.n_seqs, b.n_tokens)
@@ -1308,20 +1198,23 @@ Plan make_plan(const kvc_paged_desc &p, const kvc_paged_batch &b) {
       steps = (steps + 1) / 2;
     }
     if (w.whole) {
-      // each row tile once; a batch of single tokens needs no search for it
-      w.grid = (uint32_t)(b.q_start ? std::min<uint64_t>(units, 4 * slots) : units);
+      w.grid = (uint32_t)units;
     } else {
       w.grid = (uint32_t)std::min<uint64_t>(slots, (units * steps + min_steps(w) - 1) / min_steps(w));
       w.join = true;
-      w.by_unit = !b.q_start && units < w.grid;
+      w.by_unit = units < w.grid;
       w.infos = w.by_unit ? units : w.grid;
       parts = 2ull * w.grid * w.wg_heads;
     }
   } else {
-    // Equal splits of every row tile: as many as make the workgroups come out
-    // in whole rounds, at least 256 tokens to a split.
+    // Equal splits of every row tile, of 256 tokens at least, if the tiles do
+    // not fill the chip.  (More, for the sake of uneven lengths, cost more in
+    // parts and their join than they gain: with three times as many, 48
+    // sequences of 400 to 12,150 tokens and two new ones each took 294 us
+    // instead of 331, but 64 equal ones 246 instead of 187.)
     const uint64_t most = std::max<uint64_t>(1, ((uint64_t)b.max_len + 255) / 256);
-    w.splits = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(slots * 128 / w.rows / units, most));
+    w.splits = (uint32_t)std::max<uint64_t>(
+        1, std::min<uint64_t>(slots * 128 / w.rows / units, most));
     w.join = w.splits > 1;
     parts = w.join ? units * w.splits : 0;
   }
@@ -1338,13 +1231,9 @@ template <class TI, class TC, int D>
 hipError_t launch_d(const AttendArgs &a, const Plan &w, hipStream_t stream) {
   const uint32_t units = w.tiles * a.n_kv_heads;
   if (w.rows == 16) {
-    if (a.s.q_start)
-      hipLaunchKernelGGL((k_attend_rows<TI, TC, D, false>), dim3(w.grid), dim3(256), 0, stream, a);
-    else
-      hipLaunchKernelGGL((k_attend_rows<TI, TC, D, true>), dim3(w.grid), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((k_attend_rows<TI, TC, D>), dim3(w.grid), dim3(256), 0, stream, a);
     if (w.join) {
-      const dim3 grid((uint32_t)w.infos, a.s.q_start ? kRowTile : std::min(kRowTile, a.group),
-                      w.wg_heads);
+      const dim3 grid((uint32_t)w.infos, std::min(kRowTile, a.group), w.wg_heads);
       if ((uint64_t)grid.x * grid.y * grid.z <= 2 * kCus)
         hipLaunchKernelGGL((k_attend_rows_join<TI, TC, D, 16>), grid, dim3(1024), 0, stream, a);
       else
@@ -1391,6 +1280,7 @@ hipError_t launch_attend(const kvc_paged_desc &p, const kvc_paged_batch &b, Atte
   const Plan w = make_plan(p, b);
   a.splits = w.splits;
   a.whole = w.whole;
+  a.seq_tiles = (a.group + kRowTile - 1) / kRowTile;
   a.step_shift = w.shift;
   a.by_unit = w.by_unit;
   a.pieces = w.grid;

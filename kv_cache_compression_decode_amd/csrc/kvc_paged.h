@@ -156,6 +156,7 @@ struct AttendArgs {
   uint32_t n_heads, n_kv_heads, group;
   FastDiv group_div;
   uint32_t splits;     // of the kernel for prompts
+  uint32_t seq_tiles;  // row tiles of a sequence and KV head (16-row kernel)
   uint32_t step_shift;  // log2 of the tokens of a step of the 16-row kernel, at least 5
   uint32_t min_steps;  // of the 16-row kernel: steps a workgroup takes at least
   uint32_t pieces;     // its workgroups
