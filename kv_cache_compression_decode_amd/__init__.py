@@ -961,8 +961,9 @@ def append_async(desc: PagedDesc, batch: PagedBatch, layer: int, pool: torch.Ten
         os_ = _token_rows(q_out, n, heads, dim, dtype, dev, "q_out")
     if rope is not None and rope.cos_sin.device != dev:
         raise ValueError("the rotation table must be on the batch's device")
-    _check(lib().kvc_append(desc, batch._args(desc, n), layer, _pool_ptr(desc, pool, dev), k.data_ptr(), ks,
-                            v.data_ptr(), vs, None if q is None else q.data_ptr(), qs,
+    _check(lib().kvc_append(desc, batch._args(desc, n), layer, _pool_ptr(desc, pool, dev),
+                            k.data_ptr(), ks, v.data_ptr(), vs,
+                            None if q is None else q.data_ptr(), qs,
                             None if q is None else q_out.data_ptr(), os_,
                             None if rope is None else rope._args(), wsp.status.data_ptr(),
                             _paged_stream(stream, dev)), "kvc_append")

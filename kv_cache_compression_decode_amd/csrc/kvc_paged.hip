@@ -176,13 +176,14 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
   const bool turn = a.rotary != 0;
   const uint32_t item = blockIdx.y * 256u + threadIdx.x;
   if (item < a.k_items) {
-    append_item<TI, TC, kStream>(a, a.k + row * a.k_stride, a.k_cache + (uint64_t)slot * a.row, item, turn, cs);
+    append_item<TI, TC, kStream>(a, a.k + row * a.k_stride, a.k_cache + (uint64_t)slot * a.row,
+                                 item, turn, cs);
   } else if (item < 2 * a.k_items) {
-    append_item<TI, TC, kStream>(a, a.v + row * a.v_stride, a.v_cache + (uint64_t)slot * a.row, item - a.k_items,
-                        false, cs);
+    append_item<TI, TC, kStream>(a, a.v + row * a.v_stride, a.v_cache + (uint64_t)slot * a.row,
+                                 item - a.k_items, false, cs);
   } else if (item < 2 * a.k_items + a.q_items) {
     append_item<TI, TI, kStream>(a, a.q + row * a.q_stride, a.q_out + row * a.q_out_stride,
-                        item - 2 * a.k_items, turn, cs);
+                                 item - 2 * a.k_items, turn, cs);
   }
 }
 

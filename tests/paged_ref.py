@@ -80,7 +80,8 @@ def attend(q, k, v, pos, scale, window, cache_dtype, out_dtype):
             tail = 2.0 ** -39 * w.amax(-1, keepdim=True)
             a = (((w * (rel + mean) + tail)[..., None]) * vv.abs()[None]).sum(1)
             o = out[i, j * g:(j + 1) * g]
-            b_out[i, j * g:(j + 1) * g] = a * 1.01 + half_step(out_dtype) * (o.abs() + a) + 2.0 ** -25
+            b_out[i, j * g:(j + 1) * g] = (a * 1.01 + half_step(out_dtype) * (o.abs() + a)
+                                           + 2.0 ** -25)
             b_lse[i, j * g:(j + 1) * g] = (ds.amax(-1) + (2 * cnt + 8) * F32
                                            + 8 * F32 * (e[:, 0].abs() + 40))
     return out, lse, b_out, b_lse

@@ -188,7 +188,8 @@ HOST = r"""
 #include <cstdlib>
 #include "kvc_paged.h"
 using namespace kvc;
-#define CHECK(x) do { if (!(x)) { std::printf("failed: %s, line %d\n", #x, __LINE__); return 1; } } while (0)
+#define CHECK(x) \
+  do { if (!(x)) { std::printf("failed: %s, line %d\n", #x, __LINE__); return 1; } } while (0)
 int main() {
   // the quotient, at multiples of the divisor and next to them
   uint32_t ds[] = {1, 2, 3, 5, 7, 10, 16, 20, 48, 1000, 1500, 4097, 65535, 65536, 65537,
