@@ -460,7 +460,7 @@ typedef struct {
   uint32_t n_seqs;        /* at most 2^20 */
   uint32_t table_stride;  /* entries in a row of table */
   uint32_t n_tokens;      /* rows of q, k, v, out, at most 2^20; n_seqs if q_start is NULL */
-  uint32_t max_len;       /* bound of lens, at most table_stride * page_tokens */
+  uint32_t max_len;       /* bound of lens, at most table_stride * page_tokens and 2^30 */
 } kvc_paged_batch;
 
 /*
@@ -511,7 +511,7 @@ uint64_t kvc_attend_ws_bytes(const kvc_paged_desc *p, const kvc_paged_batch *b);
  * A row without a visible token gives zeros and lse = -infinity; what lies
  * in hidden tokens (infinities and NaN included) has no effect.  out:
  * [n_tokens][n_heads][head_dim] with out_stride elements from one token to
- * the next; lse: [n_tokens][n_heads] binary32, or NULL.  The new tokens' own
+ * the next (alignment as for kvc_append; out may be q itself); lse: [n_tokens][n_heads] binary32, or NULL.  The new tokens' own
  * keys and values are read from the pool (kvc_append first).
  */
 kvc_status kvc_attend(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t layer,

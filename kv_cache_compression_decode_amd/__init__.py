@@ -865,7 +865,7 @@ class PagedBatch:
         q = self.q_start
         return _PagedBatch(self.table.data_ptr(), self.lens.data_ptr(),
                            None if q is None else q.data_ptr(), self.n_seqs, self.table.shape[1],
-                           n_tokens, min(most, 2**31 - 1) if self.max_len is None
+                           n_tokens, min(most, 1 << 30) if self.max_len is None
                            else self.max_len)
 
 

@@ -266,7 +266,7 @@ kvc_status batch_sizes(const kvc_paged_desc *p, const kvc_paged_batch *b) {
   // one block per row or row tile: launch grids below 2^32 threads
   if (b->n_seqs > (1u << 20) || b->n_tokens > (1u << 20)) return KVC_ERR_SHAPE;
   if (!b->q_start && b->n_tokens != b->n_seqs) return KVC_ERR_SHAPE;
-  if (b->max_len >= (1u << 31)) return KVC_ERR_SHAPE;
+  if (b->max_len > (1u << 30)) return KVC_ERR_SHAPE;  // a tile's end stays in 31 bits
   if (b->n_seqs && b->max_len > (uint64_t)b->table_stride * p->page_tokens) return KVC_ERR_SHAPE;
   return KVC_OK;
 }

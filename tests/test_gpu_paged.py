@@ -146,7 +146,7 @@ PROMPT = [
     (4, 4, 128, 16, BF16, BF16, [130, 1, 200], [130, 1, 129], 0),
     (16, 2, 128, 16, BF16, F16, [600, 64, 311], [37, 64, 300], 0),
     (14, 2, 96, 20, F16, F16, [150, 300], [150, 41], 50),
-    (12, 1, 256, 10, BF16, BF16, [90, 257], [90, 20], 0),
+    (11, 1, 256, 10, BF16, BF16, [90, 257], [90, 20], 0),
     (3, 3, 256, 64, F16, F16, [200], [131], 1),
     (6, 6, 64, 1, F16, F16, [70, 3, 65], [70, 0, 64], 7),
     (64, 1, 64, 32, BF16, F16, [129], [9], 0),
@@ -260,7 +260,7 @@ APPEND = [
     (8, 8, 64, 16, BF16, BF16, [64, 33], [64, 20], 64, True),
     (4, 2, 96, 20, BF16, F16, [50, 3, 21], [50, 0, 21], 48, False),
     (4, 2, 96, 1, F16, F16, [50, 3, 21], [1, 2, 3], 32, True),
-    (6, 3, 256, 7, BF16, F16, [30], [30], 16, False),
+    (9, 3, 256, 7, BF16, F16, [30], [30], 16, False),
     (2, 1, 64, 1500, F16, F16, [1600], [1503], 0, False),
 ]
 
@@ -470,7 +470,7 @@ def test_q_start_that_overlaps_itself(heads):
     assert int(st.wsp.status.item()) == kvc.ERR_SHAPE
 
 
-def test_binding_refuses_what_it_cannot_pass_on():
+def test_binding_refuses_what_it_cannot_pass_on(monkeypatch):
     st = Setup([40], [1], 4, 2, 64, 16, F16, F16, single=True)
     out = torch.empty_like(st.q.contiguous())
     flat = torch.zeros((2, 2, 50, 128), dtype=F16, device=DEV)
@@ -499,10 +499,20 @@ def test_binding_refuses_what_it_cannot_pass_on():
         kvc.PagedBatch(st.table, st.lens.to(torch.int64))
     with pytest.raises(ValueError):
         kvc.make_paged_desc(1, 8, 2, 64 + (1 << 32), 16, 4)
+    with monkeypatch.context() as m:  # as on a box where another device is current
+        m.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+        with pytest.raises(ValueError):
+            attend()
     small = kvc.PagedWorkspace(st.desc, st.batch)
     long = kvc.PagedBatch(torch.zeros((1, 4), dtype=torch.int32, device=DEV), st.lens, max_len=64)
-    attend()  # and a good call still goes through
+    attend()  # and a good call still goes through, on a pool of bit patterns too
     assert int(st.wsp.status.item()) == 0
+    want = out.clone()
+    attend(pool=st.pool.view(torch.int16))
+    assert torch.equal(out, want)
+    q = st.q.clone()
+    attend(q=q, out=q)  # the queries' own place
+    assert torch.equal(q, want)
     big = kvc.make_paged_desc(2, 4, 2, 64, 1 << 20, 4)
     pool = torch.zeros((1,), dtype=F16, device=DEV)
     with pytest.raises(ValueError):

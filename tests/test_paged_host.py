@@ -91,6 +91,7 @@ BATCH_BAD = [
     (dict(n_seqs=(1 << 20) + 1, n_tokens=(1 << 20) + 1), SHAPE),
     (dict(n_tokens=4), SHAPE),
     (dict(max_len=161), SHAPE),
+    (dict(table_stride=1 << 27, max_len=(1 << 30) + 1), SHAPE),
     (dict(lens=None), INVALID), (dict(table=None), INVALID), (dict(lens=A + 2), INVALID),
     (dict(table=A + 1), INVALID), (dict(q_start=A + 2), INVALID),
     (dict(q_start=A, n_tokens=(1 << 20) + 1), SHAPE)]
