@@ -143,15 +143,15 @@ __device__ inline bool nonfinite2(uint32_t w) {
 }
 
 // ---------------------------------------------------- sharing out the tokens
-// One new token a sequence: the work of a call is a line of steps (a tile of 32
-// tokens for one row tile and KV head; more tiles where a call's steps would
-// pass 31 bits): head by head, in each the row tiles in sequence order, in each
-// its tokens.  The line is cut into equal pieces, one to a workgroup, wherever
-// the cuts fall, so workgroups finish together however uneven the lengths are
-// (20 sequences of 1,000 to 8,900 tokens: 6.2 TB/s).  A workgroup that holds
-// all of a row tile's steps writes its rows' outputs; one that holds a part
-// writes its sums, maxima and unnormalised output to the workspace (at most
-// two parts, at its piece's two ends) and k_attend_rows_join adds them up.
+// One new token a sequence, up to 16 query heads to a KV head: the work of a
+// call is a line of steps (a tile of 32 tokens of one KV head; more tiles where
+// a call's steps would pass 31 bits): head by head, in each the sequences, in
+// each its tokens.  The line is cut into equal pieces, one to a workgroup,
+// wherever the cuts fall, so workgroups finish together however uneven the
+// lengths are (20 sequences of 1,000 to 8,900 tokens: 6.2 TB/s).  A workgroup
+// that holds all of a sequence's steps writes its rows' outputs; one that holds
+// a part writes its sums, maxima and unnormalised output to the workspace (at
+// most two parts, at its piece's two ends) and k_attend_rows_join adds them up.
 //
 // A workgroup's four waves take four neighbouring KV heads of the same tokens
 // where there are so many (two and two, or one, otherwise: then the waves of
@@ -159,8 +159,9 @@ __device__ inline bool nonfinite2(uint32_t w) {
 // are short, and four side by side are fetched from HBM a tenth faster than
 // four rows of one head.  "Head" below is such a group of a.wg_heads heads.
 //
-// Where no cache is longer than a few steps (`whole`), every row tile counts
-// as one step, is never cut, and needs no join.
+// Where no cache is longer than a few steps (`whole`), every workgroup takes a
+// sequence and head as a whole, and nothing needs a join; there may then be
+// more than 16 query heads, in row tiles of 16.
 
 // Workgroups that the 256 CUs hold at once (by registers): the pieces at most.
 constexpr uint32_t kCus = 256;
@@ -169,10 +170,10 @@ constexpr uint32_t kRowTile = 16;
 constexpr uint32_t kTok = 32;
 
 struct Work {
-  uint32_t b, k;  // the sequence and its row tile
+  uint32_t b;  // the sequence
   int32_t len;
 
-  // steps of a row tile of a sequence: at least one, so that every row is written
+  // steps of a sequence: at least one, so that every row is written
   __device__ static uint32_t steps_of(const AttendArgs &a, int32_t len) {
     if (a.whole) return 1;
     const int32_t n = len - first_of(a, len);
@@ -186,10 +187,8 @@ struct Work {
     b = seq;
     len = a.s.len(b);
   }
-  // the next row tile; after the last sequence's, the first one's (next head)
+  // the next sequence; after the last one, the first one's next head
   __device__ void next(const AttendArgs &a, uint32_t &head) {
-    if (++k < a.seq_tiles) return;
-    k = 0;
     uint32_t s = b + 1;
     if (s == a.s.n_seqs) {
       s = 0;
@@ -225,9 +224,7 @@ struct Steps {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       bad = bad || a.s.len_out(len[i]);
-      w[i] = b0 + lane * 4 + i < a.s.n_seqs
-                 ? a.seq_tiles * Work::steps_of(a, a.s.clamp_len(len[i]))
-                 : 0;
+      w[i] = b0 + lane * 4 + i < a.s.n_seqs ? Work::steps_of(a, a.s.clamp_len(len[i])) : 0;
       sum += w[i];
     }
     if (check && bad) set_status(a.status, KVC_ERR_SHAPE);
@@ -246,13 +243,13 @@ struct Pieces {
   }
 };
 
-// What the workgroup that holds a row tile's first part leaves for the join:
-// whether there are others, and which workgroups hold them.  One for each
-// workgroup (whose last part alone can be cut and the first of its row tile),
-// or, where there are fewer row tiles than that, one for each row tile and
-// head (`by_unit`), so that the join launches no idle workgroups.
+// What the workgroup that holds a sequence's first part (of a head) leaves for
+// the join: whether there are others, and which workgroups hold them.  One for
+// each workgroup (whose last part alone can be cut and the first of its
+// sequence), or, where sequences and heads are fewer, one for each of those
+// (`by_unit`), so that the join launches no idle workgroups.
 struct JoinInfo {
-  uint32_t cut, b, k, head, first, last, slot, pad;
+  uint32_t cut, b, head, first, last, slot, pad[2];
 };
 
 // ------------------------------------------------- one new token a sequence
@@ -286,14 +283,15 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
   // this workgroup's piece of the line, and where it begins
   Work u;
   uint32_t hg;
-  uint32_t at, stop, off;  // off: steps of the first row tile before the piece
+  uint32_t row_tile = 0;
+  uint32_t at, stop, off;  // off: steps of the first sequence before the piece
   Pieces pc{gridDim.x, 1, 0};
   JoinInfo *info = static_cast<JoinInfo *>(a.info);
   if (a.whole) {  // a row tile to a workgroup: no search
     const uint32_t unit = blockIdx.x / a.head_groups;
     hg = blockIdx.x - unit * a.head_groups;
     u.load(a, unit / a.seq_tiles);
-    u.k = unit - u.b * a.seq_tiles;
+    row_tile = unit - u.b * a.seq_tiles;
     at = off = 0;
     stop = 1;
     if (threadIdx.x == 0 && a.s.len_bad(u.b)) set_status(a.status, KVC_ERR_SHAPE);
@@ -341,9 +339,6 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
           ++b;
         }
       u.load(a, b);
-      const uint32_t steps = Work::steps_of(a, u.len);
-      u.k = min(x / steps, a.seq_tiles - 1);
-      x -= u.k * steps;
       break;
     }
     off = x;
@@ -357,10 +352,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
   const uint32_t my_head = wave / turns, turn = wave - my_head * turns;
   while (at < stop && hg < a.head_groups) {
     const uint32_t hk = hg * a.wg_heads + my_head;
-    // the part of row tile u.k that this workgroup holds: steps [s_lo, s_hi)
+    // the part of sequence u.b that this workgroup holds: steps [off, off + left)
     const uint32_t steps = Work::steps_of(a, u.len);
     const uint32_t left = min(steps - off, stop - at);
-    const uint32_t first = u.k * kRowTile, rows = min(kRowTile, a.group - first);
+    const uint32_t first = row_tile * kRowTile, rows = min(kRowTile, a.group - first);
     const bool live = n16 < rows;
     const int32_t begin = Work::first_of(a, u.len), end = u.len;
     const int32_t tiles = end > begin ? (int32_t)(((uint32_t)(end - begin) + kTok - 1) / kTok) : 0;
@@ -573,10 +568,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
     }
     if (threadIdx.x == 0 && off == 0 && info) {
       const bool cut = left < steps;
-      const uint32_t id =
-          a.by_unit ? (u.b * a.seq_tiles + u.k) * a.head_groups + hg : blockIdx.x;
+      const uint32_t id = a.by_unit ? u.b * a.head_groups + hg : blockIdx.x;
       if (cut)
-        info[id] = JoinInfo{1, u.b, u.k, hg, blockIdx.x, pc.owner(at + steps - 1), slot, 0};
+        info[id] = JoinInfo{1, u.b, hg, blockIdx.x, pc.owner(at + steps - 1), slot, {0, 0}};
       else if (a.by_unit)
         info[id].cut = 0;
     }
@@ -590,7 +584,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
   if (__ballot(bad) && lane == 0) set_status(a.status, KVC_ERR_SHAPE);
 }
 
-// Joins the parts of a row tile that k_attend_rows cut: a workgroup for each
+// Joins the parts of a sequence that k_attend_rows cut: a workgroup for each
 // JoinInfo, row and head of the group.  Its W waves share the parts and are
 // added up through LDS in a fixed order: 16 waves where there are few rows to
 // join and so many parts to each, 4 otherwise.
@@ -604,7 +598,7 @@ __global__ __launch_bounds__(W * 64) void k_attend_rows_join(AttendArgs a) {
   if (info.cut != 1 || info.b >= a.s.n_seqs || info.first > info.last || info.last >= a.pieces)
     return;
   const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = blockIdx.y;
-  if (info.k * kRowTile + r >= a.group || info.head >= a.head_groups) return;
+  if (info.head >= a.head_groups) return;
   const uint32_t parts = info.last - info.first + 1;
   auto part_of = [&](uint32_t i) {
     return ((uint64_t)(info.first + i) * 2 + (i == 0 ? info.slot : 0)) * a.wg_heads + blockIdx.z;
@@ -673,7 +667,7 @@ __global__ __launch_bounds__(W * 64) void k_attend_rows_join(AttendArgs a) {
   for (uint32_t w = 0; w < W; ++w) l += s_l[w];
   const bool some = len > 0;
   const float inv = some ? 1.0f / l : 0.0f;
-  const uint32_t h = (info.head * a.wg_heads + blockIdx.z) * a.group + info.k * kRowTile + r;
+  const uint32_t h = (info.head * a.wg_heads + blockIdx.z) * a.group + r;
   TI *out = static_cast<TI *>(a.out) + (uint64_t)info.b * a.out_stride + (uint64_t)h * D;
   if (threadIdx.x < D / 2) {
     const uint32_t x = threadIdx.x * 2;
@@ -1158,8 +1152,8 @@ struct Plan {
   uint32_t rows;      // 16, 128 or 256 to a workgroup
   uint32_t grid;      // workgroups of the 16-row kernel
   uint32_t wg_heads;  // KV heads to one of them
-  bool whole, join;   // it cuts no row tile; a second launch is needed
-  bool by_unit;       // JoinInfo records: one for each row tile and KV head
+  bool whole, join;   // it cuts nothing; a second launch is needed
+  bool by_unit;       // JoinInfo records: one for each sequence and head
   uint64_t infos;
   uint32_t shift;     // log2 of the tokens of a step
   uint32_t tiles, splits;             // of k_attend_tile
@@ -1177,24 +1171,29 @@ Plan make_plan(const kvc_paged_desc &p, const kvc_paged_batch &b) {
   if (b.n_seqs == 0 || b.n_tokens == 0) return w;
   const uint32_t group = p.n_heads / p.n_kv_heads;
   const uint32_t slots = resident(p.head_dim);
-  // Several tokens go to the tile kernel however few they are (8 sequences of
-  // 4 tokens and 8 heads to a KV head, 8,000 in the cache: 67 us against 99
-  // for 16-row tiles, which read a cache once for every 16 rows); with 256-row
-  // tiles (keys and values fetched half as often, on average half a tile of a
-  // sequence empty) from 1,024 rows a sequence on.
+  // The 16-row kernel reads a cache once for every 16 rows.  Several tokens go
+  // to the tile kernel however few they are (8 sequences of 4 tokens and 8
+  // heads to a KV head, 8,000 in the cache: 67 us against 99 for 16-row tiles),
+  // and so do single ones with more than 16 heads to a KV head unless caches
+  // are short (64 sequences of 8,000, 64 heads to one KV head: 66 us against
+  // 159; 20 heads, 300 tokens: 20 against 15).  256-row tiles (keys and values
+  // fetched half as often, on average half a tile of a sequence empty) are
+  // taken from 1,024 rows a sequence on.
+  const uint64_t steps32 = std::max<uint64_t>(1, ((uint64_t)b.max_len + kTok - 1) / kTok);
+  w.whole = !b.q_start && steps32 <= kWholeSteps;
   const uint64_t avg = b.q_start ? (uint64_t)b.n_tokens * group / b.n_seqs : 0;
-  w.rows = !b.q_start ? 16 : avg < 1024 || p.head_dim == 256 ? 128 : 256;
+  w.rows = !b.q_start ? (group <= 16 || w.whole ? 16 : 128)
+           : avg < 1024 || p.head_dim == 256 ? 128 : 256;
   // every sequence's last tile may be partly filled
-  w.tiles = b.q_start ? (uint32_t)((uint64_t)b.n_tokens * group / w.rows) +
-                            std::min(b.n_seqs, b.n_tokens)
-                      : b.n_seqs * ((group + 15) / 16);
+  w.tiles = w.rows == 16 ? b.n_seqs * ((group + 15) / 16)
+                         : (uint32_t)((uint64_t)b.n_tokens * group / w.rows) +
+                               std::min(b.n_seqs, b.n_tokens);
   w.wg_heads = p.n_kv_heads % 4 == 0 ? 4 : p.n_kv_heads % 2 == 0 ? 2 : 1;
   if (w.rows != 16) w.wg_heads = 1;
   const uint64_t units = (uint64_t)w.tiles * (p.n_kv_heads / w.wg_heads);
   uint64_t parts = 0;
   if (w.rows == 16) {
-    uint64_t steps = std::max<uint64_t>(1, ((uint64_t)b.max_len + kTok - 1) / kTok);
-    w.whole = steps <= kWholeSteps;
+    uint64_t steps = steps32;
     w.shift = 5;
     while (!w.whole && units * steps >= (1ull << 31)) {
       ++w.shift;

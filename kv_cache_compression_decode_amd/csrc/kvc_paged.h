@@ -163,7 +163,7 @@ struct AttendArgs {
   uint32_t wg_heads;   // KV heads to one of them (1, 2 or 4)
   uint32_t head_groups;
   bool by_unit;        // the layout of its join records
-  bool whole;          // the 16-row kernel cuts no row tile
+  bool whole;          // the 16-row kernel takes sequences as a whole
   float scale;      // scale * log2(e)
   uint32_t window;
   int32_t *status;

@@ -130,6 +130,10 @@ SINGLE = [
     (12, 6, 64, 16, F16, F16, [700, 33, 1025, 0, 2], 0),
     (68, 4, 96, 7, BF16, BF16, [640, 800, 31], 500),
     (8, 8, 256, 16, F16, F16, [900, 513], 0),
+    # more than 16 heads to a KV head over long caches and short ones
+    (66, 2, 128, 16, BF16, BF16, [700, 0, 1, 65, 1300], 0),
+    (128, 1, 256, 10, F16, F16, [600, 90], 130),
+    (40, 2, 96, 16, BF16, F16, [400, 1, 0, 33], 60),
 ]
 
 
