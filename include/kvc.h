@@ -511,8 +511,9 @@ uint64_t kvc_attend_ws_bytes(const kvc_paged_desc *p, const kvc_paged_batch *b);
  * A row without a visible token gives zeros and lse = -infinity; what lies
  * in hidden tokens (infinities and NaN included) has no effect.  out:
  * [n_tokens][n_heads][head_dim] with out_stride elements from one token to
- * the next (alignment as for kvc_append; out may be q itself); lse: [n_tokens][n_heads] binary32, or NULL.  The new tokens' own
- * keys and values are read from the pool (kvc_append first).
+ * the next (alignment as for kvc_append; out may be q itself); lse:
+ * [n_tokens][n_heads] binary32, or NULL.  The new tokens' own keys and
+ * values are read from the pool (kvc_append first).
  */
 kvc_status kvc_attend(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t layer,
                       const void *pool, const void *q, uint64_t q_stride, float scale,
