@@ -926,6 +926,11 @@ def _token_rows(t: torch.Tensor, n: int, heads: int, dim: int, dtype, device, wh
     return s[0] if n > 1 else heads * dim
 
 
+def _workspace_check(wsp: PagedWorkspace, device) -> None:
+    if wsp.ws.device != device or wsp.status.device != device:
+        raise ValueError("the workspace must be on the batch's device")
+
+
 def _paged_stream(stream: Optional[torch.cuda.Stream], device):
     """_stream for a step's many small calls: the current stream's handle
     without a Stream object."""
@@ -961,6 +966,7 @@ def append_async(desc: PagedDesc, batch: PagedBatch, layer: int, pool: torch.Ten
         os_ = _token_rows(q_out, n, heads, dim, dtype, dev, "q_out")
     if rope is not None and rope.cos_sin.device != dev:
         raise ValueError("the rotation table must be on the batch's device")
+    _workspace_check(wsp, dev)
     _check(lib().kvc_append(desc, batch._args(desc, n), layer, _pool_ptr(desc, pool, dev),
                             k.data_ptr(), ks, v.data_ptr(), vs,
                             None if q is None else q.data_ptr(), qs,
@@ -981,8 +987,7 @@ def _attend(name: str, desc: PagedDesc, batch: PagedBatch, layer: int, pool, q, 
         raise ValueError("lse must be a contiguous [n_tokens][n_heads] float32 tensor")
     _u32(window, "window")
     _u32(layer, "layer")
-    if wsp.ws.device != dev:
-        raise ValueError("the workspace must be on the batch's device")
+    _workspace_check(wsp, dev)
     _check(getattr(lib(), name)(desc, batch._args(desc, n), layer, _pool_ptr(desc, pool, dev),
                                 q.data_ptr(), qs, dim ** -0.5 if scale is None else scale, window,
                                 out.data_ptr(), os_, None if lse is None else lse.data_ptr(),

@@ -266,3 +266,36 @@ def test_index_arithmetic_on_the_host(tmp_path):
                            "-I", os.path.join(ROOT, "include"), "-I", build.CSRC, str(src),
                            "-o", str(exe)])
     assert subprocess.check_output([str(exe)], text=True).strip() == "ok"
+
+
+class _HostBatch:
+    """Stands for a batch whose tensors are in host memory: the binding's
+    checks can be walked without a GPU."""
+    device = torch.device("cpu")
+    n_seqs = 1
+
+    def _args(self, desc, n):
+        return _batch(n_seqs=1, n_tokens=n)
+
+
+class _Scratch:
+    def __init__(self, ws, status):
+        self.ws, self.status = ws, status
+        self.ws_bytes = ws.numel()
+
+
+@pytest.mark.parametrize("call", ["append_async", "attend_async", "attend_prompt_async"])
+@pytest.mark.parametrize("elsewhere", ["ws", "status"])
+def test_workspace_of_another_device(call, elsewhere):
+    """A workspace or status word on another device than the batch would be
+    written through an address that means something else there."""
+    desc = _desc(n_layers=1, n_heads=4, head_dim=64, n_pages=2)
+    host = dict(ws=torch.zeros(256, dtype=torch.uint8), status=torch.zeros(1, dtype=torch.int32))
+    host[elsewhere] = host[elsewhere].to("meta")
+    wsp = _Scratch(**host)
+    pool = torch.zeros(desc.pool_shape, dtype=torch.float16)
+    q = torch.zeros((1, 4, 64), dtype=torch.float16)
+    k = torch.zeros((1, 2, 64), dtype=torch.float16)
+    args = (k, k) if call == "append_async" else (q, q.clone())
+    with pytest.raises(ValueError, match="workspace"):
+        getattr(kvc, call)(desc, _HostBatch(), 0, pool, *args, wsp)
