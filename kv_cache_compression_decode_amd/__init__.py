@@ -907,12 +907,17 @@ class Rope:
         return _RopeArgs(t.data_ptr(), t.shape[0], t.shape[1], int(self.interleaved), 0)
 
 
+def _cache_type(desc: PagedDesc, t: torch.Tensor, what: str) -> None:
+    if t.dtype != torch.int16 and t.dtype != _DTYPES[desc.cache_dtype]:
+        raise ValueError(f"the {what}'s type differs from the descriptor's (int16 holds bit "
+                         "patterns of either)")
+
+
 def _pool_ptr(desc: PagedDesc, pool: torch.Tensor, device) -> int:
     if pool.shape != desc.pool_shape or pool.device != device or not pool.is_contiguous():
         raise ValueError(f"the pool must be contiguous, of shape {desc.pool_shape}, on the "
                          "batch's device")
-    if pool.dtype != torch.int16 and pool.dtype != _DTYPES[desc.cache_dtype]:
-        raise ValueError("the pool's type differs from the descriptor's")
+    _cache_type(desc, pool, "pool")
     return pool.data_ptr()
 
 
@@ -1018,6 +1023,9 @@ def _page_args(desc: PagedDesc, pool, table, flat, status, *tokens):
     dev = pool.device
     for x in tokens:
         _u32(x, "a token position or count")
+    if flat.dim() != 4:
+        raise ValueError("the tensor must have four dimensions [L][2][T][C]")
+    _cache_type(desc, flat, "tensor")
     _int32_tensor(table, 1, "table")
     _int32_tensor(status, 1, "status")
     shape = (desc.n_layers, 2, flat.shape[2], desc.n_kv_heads * desc.head_dim)
@@ -1030,8 +1038,9 @@ def page_out_async(desc: PagedDesc, pool: torch.Tensor, table: torch.Tensor, fir
                    n_tokens: int, out: torch.Tensor, out_first: int, status: torch.Tensor,
                    stream=None) -> None:
     """Launch kvc_page_out: tokens [first_token, first_token + n_tokens) of the
-    sequence with page ids `table`, every layer, into out [L][2][T][C] from
-    token out_first on (no sync; device errors stay in status)."""
+    sequence with page ids `table`, every layer, into out [L][2][T][C] (of the
+    cache's type, or int16 bit patterns) from token out_first on (no sync;
+    device errors stay in status)."""
     dev, pp, fp = _page_args(desc, pool, table, out, status, first_token, n_tokens, out_first)
     _check(lib().kvc_page_out(desc, pp, table.data_ptr(), table.shape[0], first_token, n_tokens,
                               fp, out.shape[2], out_first, status.data_ptr(),

@@ -299,3 +299,27 @@ def test_workspace_of_another_device(call, elsewhere):
     args = (k, k) if call == "append_async" else (q, q.clone())
     with pytest.raises(ValueError, match="workspace"):
         getattr(kvc, call)(desc, _HostBatch(), 0, pool, *args, wsp)
+
+
+@pytest.mark.parametrize("cache,other", [(0, torch.bfloat16), (1, torch.float16)])
+def test_page_moves_check_the_tensors_type(cache, other):
+    """Page moves copy bits, so a tensor of the other 16-bit type (or one that
+    is not [L][2][T][C]) is refused; bit patterns go with either type."""
+    desc = _desc(n_layers=1, head_dim=64, n_pages=2, cache_dtype=cache, io_dtype=cache)
+    pool = torch.zeros(desc.pool_shape, dtype=kvc._DTYPES[cache])
+    table = torch.zeros(2, dtype=torch.int32)
+    status = torch.zeros(1, dtype=torch.int32)
+
+    def both(flat, match):
+        with pytest.raises(ValueError, match=match):
+            kvc.page_out_async(desc, pool, table, 0, 5, flat, 0, status)
+        with pytest.raises(ValueError, match=match):
+            kvc.page_in_async(desc, flat, 0, pool, table, 0, 5, status)
+
+    good = torch.zeros((1, 2, 5, 128), dtype=pool.dtype)
+    for t in (other, torch.uint16):
+        both(good.to(t), "type")
+    both(good[0, 0], "dimension")
+    # past these checks: refused for lying in host memory
+    both(good, "CUDA")
+    both(good.view(torch.int16), "CUDA")
