@@ -513,7 +513,8 @@ uint64_t kvc_attend_ws_bytes(const kvc_paged_desc *p, const kvc_paged_batch *b);
  * [n_tokens][n_heads][head_dim] with out_stride elements from one token to
  * the next (alignment as for kvc_append; out may be q itself); lse:
  * [n_tokens][n_heads] binary32, or NULL.  The new tokens' own keys and
- * values are read from the pool (kvc_append first).
+ * values are read from the pool (kvc_append first).  |scale| is at most
+ * 2.358e38, so that scale * log2(e) is finite (else KVC_ERR_INVALID_ARG).
  */
 kvc_status kvc_attend(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t layer,
                       const void *pool, const void *q, uint64_t q_stride, float scale,

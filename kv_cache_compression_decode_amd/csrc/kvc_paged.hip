@@ -341,7 +341,8 @@ kvc_status attend(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t la
   kvc_status st = batch_check(p, b, layer, pool, dev_status);
   if (st != KVC_OK) return st;
   if (prompt != (b->q_start != nullptr)) return KVC_ERR_INVALID_ARG;
-  if (!(scale > -3.0e38f && scale < 3.0e38f)) return KVC_ERR_INVALID_ARG;
+  const float scale_log2 = scale * 1.44269504088896340736f;
+  if (!(__builtin_fabsf(scale_log2) <= 3.4028234664e38f)) return KVC_ERR_INVALID_ARG;
   if ((uint64_t)b->n_tokens * p->n_heads > (1u << 23)) return KVC_ERR_SHAPE;  // launch grids
   if (b->n_seqs == 0 || b->n_tokens == 0) return KVC_OK;
   const uint64_t width = (uint64_t)p->n_heads * p->head_dim;
@@ -366,7 +367,7 @@ kvc_status attend(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t la
   a.n_kv_heads = p->n_kv_heads;
   a.group = p->n_heads / p->n_kv_heads;
   a.group_div = FastDiv::make(a.group);
-  a.scale = scale * 1.44269504088896340736f;
+  a.scale = scale_log2;
   a.window = window;
   a.status = dev_status;
   return launch_attend(*p, *b, a, ws, stream) == hipSuccess ? KVC_OK : KVC_ERR_HIP;

@@ -323,3 +323,19 @@ def test_page_moves_check_the_tensors_type(cache, other):
     # past these checks: refused for lying in host memory
     both(good, "CUDA")
     both(good.view(torch.int16), "CUDA")
+
+
+@pytest.mark.parametrize("name", ["kvc_attend", "kvc_attend_prompt"])
+def test_scales_that_pass_the_range(L, name):
+    """The kernels take scale * log2(e) in binary32, below 2^128: a scale of
+    2^128 / log2(e) = 2.3586e38 and above would make every score an infinity or NaN."""
+    q_start = A if name == "kvc_attend_prompt" else None
+    some = _batch(q_start=q_start)
+    none = _batch(n_seqs=0, n_tokens=0, q_start=q_start)  # accepted, nothing is launched
+    for s in (2.359e38, 2.9e38, 3.4e38, float("inf"), float("nan")):
+        for sign in (1.0, -1.0):
+            assert _attend(L, b=some, scale=sign * s, name=name) == INVALID
+            assert _attend(L, b=none, scale=sign * s, name=name) == INVALID
+    for s in (2.358e38, 1.0, 1e-45, 0.0):
+        for sign in (1.0, -1.0):
+            assert _attend(L, b=none, scale=sign * s, name=name) == 0
