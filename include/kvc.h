@@ -511,7 +511,8 @@ uint64_t kvc_attend_ws_bytes(const kvc_paged_desc *p, const kvc_paged_batch *b);
  * A row without a visible token gives zeros and lse = -infinity; what lies
  * in hidden tokens (infinities and NaN included) has no effect.  out:
  * [n_tokens][n_heads][head_dim] with out_stride elements from one token to
- * the next (alignment as for kvc_append; out may be q itself); lse:
+ * the next (alignment as for kvc_append; out may be q itself, with the same
+ * stride, and overlaps it in no other way); lse:
  * [n_tokens][n_heads] binary32, or NULL.  The new tokens' own keys and
  * values are read from the pool (kvc_append first).  |scale| is at most
  * 2.358e38, so that scale * log2(e) is finite (else KVC_ERR_INVALID_ARG).

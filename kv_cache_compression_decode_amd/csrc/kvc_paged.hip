@@ -348,6 +348,7 @@ kvc_status attend(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t la
   const uint64_t width = (uint64_t)p->n_heads * p->head_dim;
   if ((st = rows_check(q, q_stride, b->n_tokens, width)) != KVC_OK) return st;
   if ((st = rows_check(out, out_stride, b->n_tokens, width)) != KVC_OK) return st;
+  if (q == out && q_stride != out_stride && b->n_tokens > 1) return KVC_ERR_SHAPE;
   if (!aligned(lse, 4)) return KVC_ERR_INVALID_ARG;
   const uint64_t need = attend_ws_bytes(*p, *b);
   if (need && (!ws || !aligned(ws, 256))) return KVC_ERR_INVALID_ARG;

@@ -339,3 +339,13 @@ def test_scales_that_pass_the_range(L, name):
     for s in (2.358e38, 1.0, 1e-45, 0.0):
         for sign in (1.0, -1.0):
             assert _attend(L, b=none, scale=sign * s, name=name) == 0
+
+
+@pytest.mark.parametrize("name", ["kvc_attend", "kvc_attend_prompt"])
+def test_attention_in_place_with_two_strides(L, name):
+    """With out at q's place, row i of out must be row i of q: at another
+    stride it lies on rows whose queries are still to be read."""
+    b = _batch(q_start=A if name == "kvc_attend_prompt" else None)
+    big = 1 << 40
+    assert _attend(L, b=b, qs=2048, os_=1024, ws_bytes=big, name=name) == SHAPE
+    assert _attend(L, b=b, qs=1024, os_=1032, ws_bytes=big, name=name) == SHAPE
