@@ -41,9 +41,11 @@ def rotate_bound(y, mag, dtype):
     return half_step(dtype) * (y.abs() + 2 * F32 * mag) + 2 * F32 * mag + 2.0 ** -25
 
 
-def attend(q, k, v, pos, scale, window, cache_dtype, out_dtype):
+def attend(q, k, v, pos, scale, window, cache_dtype, out_dtype, shift=14):
     """q [n, h, d], k, v [m, hk, d] (any type), pos [n] -> out, lse and their
-    bounds, all float64.  Hidden tokens take no part, whatever they hold."""
+    bounds, all float64.  Hidden tokens take no part, whatever they hold.
+    shift: the power of two by which the kernel scales binary16 probabilities,
+    14 for single tokens in 16-row tiles, 11 in the larger tiles."""
     n, h, d = q.shape
     m, hk, _ = k.shape
     g = h // hk
@@ -76,8 +78,10 @@ def attend(q, k, v, pos, scale, window, cache_dtype, out_dtype):
             rel = 2 * ds + 8 * F32 + half_step(cache_dtype) + 2 * cnt * F32
             mean = (w * ds).sum(-1, keepdim=True) + (2 * cnt + 8) * F32
             # binary16 probabilities below the normal range: half a step of
-            # 2^-24 at a scale of 2^14, against the largest probability
-            tail = 2.0 ** -39 * w.amax(-1, keepdim=True)
+            # 2^-24 at a scale of 2^shift, against the probability at the
+            # kernel's reference, which is at most the largest one: 2^-39 of
+            # it at a shift of 14, 2^-36 at 11
+            tail = 2.0 ** (-25 - shift) * w.amax(-1, keepdim=True)
             a = (((w * (rel + mean) + tail)[..., None]) * vv.abs()[None]).sum(1)
             o = out[i, j * g:(j + 1) * g]
             b_out[i, j * g:(j + 1) * g] = (a * 1.01 + half_step(out_dtype) * (o.abs() + a)
