@@ -154,7 +154,7 @@ PROMPT = [
     (3, 3, 256, 64, F16, F16, [200], [131], 1),
     (6, 6, 64, 1, F16, F16, [70, 3, 65], [70, 0, 64], 7),
     (64, 1, 64, 32, BF16, F16, [129], [9], 0),
-    # 16-row tiles of several tokens, cut, beside sequences without new tokens
+    # a few tokens over long caches, split, beside sequences without new tokens
     (8, 2, 64, 16, F16, F16, [900, 1500, 30, 700, 5], [9, 3, 30, 0, 1], 0),
     (6, 1, 128, 20, BF16, BF16, [1201, 33, 0, 640], [17, 5, 0, 2], 300),
     (40, 2, 256, 16, BF16, F16, [800, 513], [3, 2], 0),
@@ -202,7 +202,7 @@ def test_attend_padding_rows():
     _check_attend(st, out, lse)
 
 
-@pytest.mark.parametrize("heads", [2, 8, 40])  # 16, 128 and 256 rows a workgroup
+@pytest.mark.parametrize("heads", [2, 8, 40])  # 128 (partly and well filled) and 256 rows a workgroup
 @pytest.mark.parametrize("dtype", [F16, BF16])
 def test_attend_nonfinite_hidden_values(dtype, heads):
     """Infinities and NaN in the cached rows of tokens that a row does not
@@ -459,7 +459,7 @@ def test_device_errors_are_reported():
         assert code(st) == kvc.ERR_SHAPE
 
 
-@pytest.mark.parametrize("heads", [2, 64])  # 16 rows a workgroup, and tiles
+@pytest.mark.parametrize("heads", [2, 64])  # 128 rows a workgroup
 def test_q_start_that_overlaps_itself(heads):
     """Every other sequence claims all rows: reported, and the call ends."""
     n = 600
