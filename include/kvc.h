@@ -413,7 +413,8 @@ kvc_status kvc_plan_stream(const uint64_t *chunk_bytes, uint32_t n_chunks, uint3
  * kvc_decode_multi and kvc_restore therefore write straight into a pool
  * (T_total = n_pages * page_tokens) wherever a chunk's tokens lie in
  * consecutive pages; kvc_page_in scatters a decoded tensor otherwise, and
- * kvc_page_out gathers what kvc_encode reads.
+ * kvc_page_out gathers what kvc_encode reads.  (The codec's own values are
+ * binary16: that goes for pools of KVC_F16.)
  *
  * Types: cache_dtype is the pool's element type, io_dtype that of q, k, v and
  * out; they are equal, or io_dtype is KVC_BF16 over a KVC_F16 pool (a
@@ -499,7 +500,14 @@ kvc_status kvc_append(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_
 
 /* Workspace bytes of kvc_attend and kvc_attend_prompt for a batch of these
  * sizes (n_seqs, n_tokens, max_len are read, and whether q_start is NULL).
- * 0 if the descriptor or the batch is invalid. */
+ * 0 if the descriptor or the batch is invalid.  The size is not monotone: a
+ * batch with fewer tokens, or a shorter max_len, may need more, because work
+ * that does not fill the chip is cut and joined.  No batch needs more than
+ * 65,536 * (4 * head_dim + 8) + 16,640 bytes, so one workspace of that size
+ * serves them all; a smaller one than a call needs is KVC_ERR_CAPACITY.  The
+ * workspace is 256-byte aligned, holds nothing between calls and serves one
+ * call at a time: calls that may run at once, captured ones too, need one
+ * each. */
 uint64_t kvc_attend_ws_bytes(const kvc_paged_desc *p, const kvc_paged_batch *b);
 
 /*
@@ -515,7 +523,12 @@ uint64_t kvc_attend_ws_bytes(const kvc_paged_desc *p, const kvc_paged_batch *b);
  * stride, and overlaps it in no other way); lse:
  * [n_tokens][n_heads] binary32, or NULL.  The new tokens' own keys and
  * values are read from the pool (kvc_append first).  |scale| is at most
- * 2.358e38, so that scale * log2(e) is finite (else KVC_ERR_INVALID_ARG).
+ * 2.358e38, so that scale * log2(e) is finite (else KVC_ERR_INVALID_ARG);
+ * n_tokens * n_heads at most 2^23 (else KVC_ERR_SHAPE).
+ * Scores, the softmax's sums and lse are binary32.  Each exp(s_j - lse) is
+ * rounded once to the cache's type before it multiplies a value (half a
+ * step: 2^-8 of it in bfloat16, 2^-11 in binary16), while its sum is taken
+ * before the rounding; out is rounded once to its own type.
  */
 kvc_status kvc_attend(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t layer,
                       const void *pool, const void *q, uint64_t q_stride, float scale,

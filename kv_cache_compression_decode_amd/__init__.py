@@ -872,7 +872,9 @@ class PagedBatch:
 class PagedWorkspace:
     """Scratch memory and status word of the paged calls on this batch with
     n_tokens rows of new tokens (default: one for each sequence).  Calls with
-    other sizes may need more and then raise ERR_CAPACITY."""
+    other sizes, fewer tokens among them, may need more and then raise
+    ERR_CAPACITY.  One call at a time: calls that may run at once (on two
+    streams, or in two captured graphs) need a workspace each."""
 
     def __init__(self, desc: PagedDesc, batch: PagedBatch, n_tokens: Optional[int] = None):
         b = batch._args(desc, batch.n_seqs if n_tokens is None else n_tokens)

@@ -4,6 +4,7 @@ arithmetic that the kernels share with the host: division by the page size,
 clamped rows and lengths, and slots of page tables with bad ids."""
 import ctypes
 import os
+import random
 import subprocess
 
 import pytest
@@ -349,3 +350,29 @@ def test_attention_in_place_with_two_strides(L, name):
     big = 1 << 40
     assert _attend(L, b=b, qs=2048, os_=1024, ws_bytes=big, name=name) == SHAPE
     assert _attend(L, b=b, qs=1024, os_=1032, ws_bytes=big, name=name) == SHAPE
+
+
+def test_workspace_bound(L):
+    """The header's bound over every batch of a descriptor; the size itself is
+    not monotone (a long prompt fills the chip uncut and needs nothing)."""
+    r = random.Random(5)
+    most = {}
+    for _ in range(20000):
+        d = r.choice([64, 96, 128, 256])
+        kv = r.choice([1, 2, 3, 4, 5, 8, 16, 64, 512])
+        group = r.choice([1, 2, 4, 7, 8, 16, 17, 64, 128])
+        if kv * group > 4096:
+            continue
+        n_seqs = int(2 ** r.uniform(0, 20)) if r.random() < 0.3 else r.randint(1, 600)
+        q_start = r.choice([None, A])
+        n_tokens = int(2 ** r.uniform(0, 20)) if q_start else n_seqs
+        b = _batch(n_seqs=n_seqs, n_tokens=n_tokens, q_start=q_start, table_stride=1 << 26,
+                   max_len=int(2 ** r.uniform(0, 30)))
+        need = L.kvc_attend_ws_bytes(_desc(head_dim=d, n_heads=kv * group, n_kv_heads=kv), b)
+        assert need <= 65536 * (4 * d + 8) + 16640, (d, kv, group, n_seqs, n_tokens, b.max_len)
+        most[d] = max(most.get(d, 0), need)
+    for d in (64, 96, 128):  # the bound is met, but for the join's records
+        assert most[d] >= 65536 * (4 * d + 8)
+    sizes = [L.kvc_attend_ws_bytes(_desc(n_heads=64, n_kv_heads=8), _batch(
+        n_seqs=1, n_tokens=n, q_start=A, table_stride=1000, max_len=16000)) for n in (37, 9000)]
+    assert sizes[0] > sizes[1] == 0
