@@ -461,7 +461,8 @@ typedef struct {
   uint32_t n_seqs;        /* at most 2^20 */
   uint32_t table_stride;  /* entries in a row of table */
   uint32_t n_tokens;      /* rows of q, k, v, out, at most 2^20; n_seqs if q_start is NULL */
-  uint32_t max_len;       /* bound of lens, at most table_stride * page_tokens and 2^30 */
+  uint32_t max_len;       /* bound of lens, at most table_stride * page_tokens and 2^30; the
+                             work of prompts is cut by it: near the longest length is best */
 } kvc_paged_batch;
 
 /*
