@@ -399,9 +399,10 @@ def prepare(case, seed):
         if op == "keep":
             st["status"] = torch.zeros(1, dtype=torch.int32, device=DEVICE)
             return st
-        st["wsp"] = kvc.PagedWorkspace(st["desc"], st["batch"], n_tok)
         if case["tree"]:
             st["draft"] = kvc.Tree(st["parent"], max(new))
+        st["wsp"] = kvc.PagedWorkspace(st["desc"], st["batch"], n_tok, tree=st.get("draft"))
+        if case["tree"]:
             kvc.tree_async(st["desc"], st["batch"], st["draft"], st["wsp"])
         if op == "append":
             st["rope"] = kvc.Rope(st["cos_sin"], interleaved=case["interleaved"])
