@@ -404,8 +404,11 @@ kvc_status kvc_plan_stream(const uint64_t *chunk_bytes, uint32_t n_chunks, uint3
 /*
  * Serving over a restored cache: new tokens written into it (kvc_append),
  * attention of new tokens over it (kvc_attend for one new token a sequence,
- * kvc_attend_prompt for several), and a context's tokens moved between pages
- * and a tensor of their own (kvc_page_out, kvc_page_in).
+ * kvc_attend_prompt for several; kvc_attend_sinks for both with a window's
+ * sinks), and a context's tokens moved between pages and a tensor of their own
+ * (kvc_page_out, kvc_page_in).  For drafted tokens: kvc_tree_build,
+ * kvc_append_norm, kvc_attend_tree and kvc_keep; for sequences that share
+ * pages: kvc_fork and kvc_resize.
  *
  * The pool is a KV cache in the layout of every other call,
  * [L][2][n_pages * page_tokens][C] with C = n_kv_heads * head_dim: page p is
@@ -543,6 +546,149 @@ kvc_status kvc_attend_prompt(const kvc_paged_desc *p, const kvc_paged_batch *b, 
                              uint32_t window, void *out, uint64_t out_stride, float *lse,
                              void *ws, uint64_t ws_bytes, int32_t *dev_status,
                              hipStream_t stream);
+
+/*
+ * kvc_attend (b->q_start NULL) or kvc_attend_prompt (not NULL) with sinks: the
+ * sequence's first `sinks` tokens stay visible behind the window,
+ *   j <= position and (j > position - window or j < sinks).
+ * With window 0 every token up to the position is visible and sinks has no
+ * effect.  Everything else, the workspace among it, is as there.
+ */
+kvc_status kvc_attend_sinks(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t layer,
+                            const void *pool, const void *q, uint64_t q_stride, float scale,
+                            uint32_t window, uint32_t sinks, void *out, uint64_t out_stride,
+                            float *lse, void *ws, uint64_t ws_bytes, int32_t *dev_status,
+                            hipStream_t stream);
+
+/*
+ * Norm of each head's keys and queries before the rotation:
+ *   y_d = x_d * w_d / sqrt(mean over the head of x^2 + eps).
+ * The squares' sum, the norm and the rotation are binary32 (a row whose sum of
+ * squares passes 3.4e38 comes out as zeros) and y is rounded once.
+ */
+typedef struct {
+  const float *q_weight; /* device [head_dim], 16-byte aligned; not read without queries */
+  const float *k_weight; /* device [head_dim], 16-byte aligned */
+  float eps;             /* positive and finite, not subnormal */
+  uint32_t reserved;     /* 0 */
+} kvc_head_norm;
+
+/*
+ * kvc_append with a norm of keys and queries (norm NULL: none), and with
+ * positions of their own for a tree's tokens: depth, device [n_tokens] or
+ * NULL, puts row q_start[b] + i at position lens[b] - n_b + depth instead of
+ * lens[b] - n_b + i.  Only the rotation uses it; the slot is i's.  A position
+ * that is negative or outside the rotation's table is KVC_ERR_SHAPE on the
+ * device, and that token is not written.
+ */
+kvc_status kvc_append_norm(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t layer,
+                           void *pool, const void *k, uint64_t k_stride, const void *v,
+                           uint64_t v_stride, const void *q, uint64_t q_stride, void *q_out,
+                           uint64_t q_out_stride, const kvc_rope *rope, const kvc_head_norm *norm,
+                           const int32_t *depth, int32_t *dev_status, hipStream_t stream);
+
+/*
+ * A tree of drafted tokens: each sequence's new tokens (b->q_start is not
+ * NULL) hang on one another.  parent holds, for row q_start[b] + i, the number
+ * of the new token that token i follows (less than i), or -1 if it follows the
+ * cached context.
+ */
+typedef struct {
+  const int32_t *parent; /* device [n_tokens] */
+  uint64_t *mask;        /* device [n_tokens][(max_tokens + 63) / 64]: bit t % 64 of word t / 64:
+                            the row's token follows token t, at once or through others, or is it */
+  int32_t *depth;        /* device [n_tokens]: tokens of the tree before it on its path */
+  uint32_t max_tokens;   /* of a sequence's tree at most, 1 .. 4096 */
+  uint32_t reserved;     /* 0 */
+} kvc_tree;
+
+/* Write mask and depth from parent (which no other call reads).  They hold
+ * for every step and layer that uses trees of this shape, whatever lens is.
+ * A sequence with more than max_tokens new tokens is KVC_ERR_SHAPE on the
+ * device and its rows are left as they were; so is a parent that is not
+ * before its token, which then counts as -1. */
+kvc_status kvc_tree_build(const kvc_paged_desc *p, const kvc_paged_batch *b, const kvc_tree *tree,
+                          int32_t *dev_status, hipStream_t stream);
+
+/* Workspace bytes of kvc_attend_tree; 0 if an argument is invalid. */
+uint64_t kvc_attend_tree_ws_bytes(const kvc_paged_desc *p, const kvc_paged_batch *b,
+                                  const kvc_tree *tree);
+
+/*
+ * Attention of a tree's tokens (b->q_start not NULL): the row of new token i
+ * sees the sequence's cached tokens j < lens[b] - n_b, the new tokens t < i
+ * that its mask holds, and itself; no window.  Otherwise as kvc_attend_prompt.
+ * The new tokens' keys and values are read from the pool (kvc_append_norm with
+ * the tree's depth first).  Bits behind a row's own are not read as tokens.
+ */
+kvc_status kvc_attend_tree(const kvc_paged_desc *p, const kvc_paged_batch *b,
+                           const kvc_tree *tree, uint32_t layer, const void *pool, const void *q,
+                           uint64_t q_stride, float scale, void *out, uint64_t out_stride,
+                           float *lse, void *ws, uint64_t ws_bytes, int32_t *dev_status,
+                           hipStream_t stream);
+
+/*
+ * Keep the accepted path of each sequence's tree: its new tokens path[b][0] <
+ * path[b][1] < .. (kept[b] of them) move to the places 0, 1, .. of its new
+ * tokens, in every layer, and new_lens[b] = lens[b] - n_b + kept[b].  path:
+ * device [n_seqs][path_stride], entries from kept[b] on are not read; kept and
+ * new_lens: device [n_seqs]; new_lens does not overlap lens (KVC_ERR_SHAPE).
+ * path_stride is at most 4096, 2 * n_layers * n_kv_heads * head_dim below
+ * 2^34 (else KVC_ERR_SHAPE).  A path that does not rise or leaves the tree, or
+ * a bad page, stores KVC_ERR_SHAPE; that sequence then stays as it is, with
+ * new_lens[b] = lens[b].  lens[b] = 0 is an unused slot: new_lens[b] = 0.
+ * The keys keep the positions that they were rotated to: on a path from the
+ * root, whose i-th token has depth i, these are the new ones.
+ */
+kvc_status kvc_keep(const kvc_paged_desc *p, const kvc_paged_batch *b, void *pool,
+                    const int32_t *path, uint32_t path_stride, const int32_t *kept,
+                    int32_t *new_lens, int32_t *dev_status, hipStream_t stream);
+
+/*
+ * The pages that sequences hold, counted on the device.  Row r of table holds
+ * the first ceil(lens[r] / page_tokens) entries' pages, and refs[page] counts
+ * the rows that hold it: 0 is a free page.  Several rows may hold a page (a
+ * forked sequence's shared beginning).  kvc_fork and kvc_resize keep the three
+ * arrays in line; table and lens may be a batch's.
+ */
+typedef struct {
+  int32_t *table;        /* device [n_rows][table_stride] */
+  int32_t *lens;         /* device [n_rows]: at most table_stride * page_tokens and 2^30 */
+  int32_t *refs;         /* device [n_pages] */
+  uint32_t n_rows;       /* at most 2048 */
+  uint32_t table_stride;
+} kvc_ledger;
+
+/*
+ * Fork sequences: row dst[i] gives up what it holds and takes row src[i]'s
+ * pages and length, for i < n (at most 2048; src, dst: device [n]).  No token
+ * is copied: kvc_resize does that when a row grows.  src[i] < 0 leaves fork i
+ * out.  Forks whose rows are outside the table or get in each other's way (a
+ * dst that stands twice, or is a src too) are left out and store
+ * KVC_ERR_SHAPE, as are rows with a bad length; so does a page id outside the
+ * pool or the release of a free page, which is passed over.
+ */
+kvc_status kvc_fork(const kvc_paged_desc *p, const kvc_ledger *g, const int32_t *src,
+                    const int32_t *dst, uint32_t n, int32_t *dev_status, hipStream_t stream);
+
+/* Workspace bytes of kvc_resize; 0 if the descriptor is invalid. */
+uint64_t kvc_resize_ws_bytes(const kvc_paged_desc *p);
+
+/*
+ * Bring every row to new_lens[r] tokens (device [n_rows]; lens becomes it).
+ * First rows that shrink give up the pages they no longer reach (all of them
+ * at 0).  Then, row by row, a row that grows from inside a page that others
+ * hold too takes a page of its own in its place, into which that page's tokens
+ * up to the old length are copied, in every layer (copy on write); and a page
+ * for each entry that it newly reaches.  Free pages are taken lowest id first.
+ * If they do not suffice, no row grows: KVC_ERR_CAPACITY on the device.  A row
+ * whose lengths are negative or above table_stride * page_tokens stays as it
+ * is: KVC_ERR_SHAPE, as for bad pages (see kvc_fork).  ws: kvc_resize_ws_bytes
+ * bytes, 256-byte aligned, one call at a time.
+ */
+kvc_status kvc_resize(const kvc_paged_desc *p, const kvc_ledger *g, const int32_t *new_lens,
+                      void *pool, void *ws, uint64_t ws_bytes, int32_t *dev_status,
+                      hipStream_t stream);
 
 /*
  * Copy tokens [first_token, first_token + n_tokens) of one sequence, every

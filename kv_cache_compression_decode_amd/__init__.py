@@ -42,7 +42,9 @@ EXPORTED = (
     "kvc_refine_profile_ws_bytes", "kvc_profile_refine", "kvc_encode_refine_ws_bytes",
     "kvc_encode_refine", "kvc_decode_refined_ws_bytes", "kvc_decode_refined",
     "kvc_validate_paged_desc", "kvc_append", "kvc_attend_ws_bytes", "kvc_attend",
-    "kvc_attend_prompt", "kvc_page_out", "kvc_page_in",
+    "kvc_attend_prompt", "kvc_page_out", "kvc_page_in", "kvc_attend_sinks", "kvc_append_norm",
+    "kvc_tree_build", "kvc_attend_tree_ws_bytes", "kvc_attend_tree", "kvc_keep", "kvc_fork",
+    "kvc_resize_ws_bytes", "kvc_resize",
 )
 
 
@@ -169,6 +171,38 @@ class _RopeArgs(ctypes.Structure):
     ]
 
 
+class _HeadNormArgs(ctypes.Structure):
+    """kvc_head_norm."""
+    _fields_ = [
+        ("q_weight", ctypes.c_void_p),
+        ("k_weight", ctypes.c_void_p),
+        ("eps", ctypes.c_float),
+        ("reserved", ctypes.c_uint32),
+    ]
+
+
+class _TreeArgs(ctypes.Structure):
+    """kvc_tree."""
+    _fields_ = [
+        ("parent", ctypes.c_void_p),
+        ("mask", ctypes.c_void_p),
+        ("depth", ctypes.c_void_p),
+        ("max_tokens", ctypes.c_uint32),
+        ("reserved", ctypes.c_uint32),
+    ]
+
+
+class _LedgerArgs(ctypes.Structure):
+    """kvc_ledger."""
+    _fields_ = [
+        ("table", ctypes.c_void_p),
+        ("lens", ctypes.c_void_p),
+        ("refs", ctypes.c_void_p),
+        ("n_rows", ctypes.c_uint32),
+        ("table_stride", ctypes.c_uint32),
+    ]
+
+
 def make_desc(n_layers: int, n_channels: int,
               delta_bits: Sequence[Sequence[int]] = ((6, 5, 4),),
               group_tokens: int = 10, chunk_tokens: int = 1500) -> CodecDesc:
@@ -256,6 +290,29 @@ def lib():
         getattr(L, name).argtypes = [pd, pb, u32, vp, vp, u64, ctypes.c_float, u32, vp, u64, vp,
                                      vp, u64, vp, vp]
         getattr(L, name).restype = ctypes.c_int
+    L.kvc_attend_sinks.argtypes = [pd, pb, u32, vp, vp, u64, ctypes.c_float, u32, u32, vp, u64,
+                                   vp, vp, u64, vp, vp]
+    L.kvc_attend_sinks.restype = ctypes.c_int
+    pt, pg = ctypes.POINTER(_TreeArgs), ctypes.POINTER(_LedgerArgs)
+    L.kvc_append_norm.argtypes = [pd, pb, u32, vp, vp, u64, vp, u64, vp, u64, vp, u64,
+                                  ctypes.POINTER(_RopeArgs), ctypes.POINTER(_HeadNormArgs), vp,
+                                  vp, vp]
+    L.kvc_append_norm.restype = ctypes.c_int
+    L.kvc_tree_build.argtypes = [pd, pb, pt, vp, vp]
+    L.kvc_tree_build.restype = ctypes.c_int
+    L.kvc_attend_tree_ws_bytes.argtypes = [pd, pb, pt]
+    L.kvc_attend_tree_ws_bytes.restype = u64
+    L.kvc_attend_tree.argtypes = [pd, pb, pt, u32, vp, vp, u64, ctypes.c_float, vp, u64, vp, vp,
+                                  u64, vp, vp]
+    L.kvc_attend_tree.restype = ctypes.c_int
+    L.kvc_keep.argtypes = [pd, pb, vp, vp, u32, vp, vp, vp, vp]
+    L.kvc_keep.restype = ctypes.c_int
+    L.kvc_fork.argtypes = [pd, pg, vp, vp, u32, vp, vp]
+    L.kvc_fork.restype = ctypes.c_int
+    L.kvc_resize_ws_bytes.argtypes = [pd]
+    L.kvc_resize_ws_bytes.restype = u64
+    L.kvc_resize.argtypes = [pd, pg, vp, vp, vp, u64, vp, vp]
+    L.kvc_resize.restype = ctypes.c_int
     L.kvc_page_out.argtypes = [pd, vp, vp, u32, u32, u32, vp, u32, u32, vp, vp]
     L.kvc_page_out.restype = ctypes.c_int
     L.kvc_page_in.argtypes = [pd, vp, u32, u32, vp, vp, u32, u32, u32, vp, vp]
@@ -871,16 +928,49 @@ class PagedBatch:
                            else self.max_len)
 
 
+class Tree:
+    """kvc_tree: a tree of drafted tokens.  parent [n_tokens] int32 on the GPU
+    holds for each new token of a sequence (the rows of batch.q_start) the
+    number of the new token of that sequence that it follows, which comes
+    before it, or -1 if it follows the cached context.  max_tokens bounds the
+    new tokens of a sequence.  tree_async fills mask [n_tokens][words] (which
+    of them each one sees: itself and what it follows) and depth [n_tokens];
+    once for every step and layer with trees of this shape."""
+
+    def __init__(self, parent: torch.Tensor, max_tokens: int):
+        self.parent = _int32_tensor(parent, 1, "parent")
+        self.max_tokens = _u32(max_tokens, "max_tokens")
+        if not 1 <= max_tokens <= 4096:
+            raise ValueError("max_tokens must be between 1 and 4096")
+        n, dev = parent.shape[0], parent.device
+        self.mask = torch.zeros((n, (max_tokens + 63) // 64), dtype=torch.int64, device=dev)
+        self.depth = torch.zeros(n, dtype=torch.int32, device=dev)
+
+    def _args(self) -> _TreeArgs:
+        return _TreeArgs(self.parent.data_ptr(), self.mask.data_ptr(), self.depth.data_ptr(),
+                         self.max_tokens, 0)
+
+    def _check(self, n: int, device) -> None:
+        if self.parent.shape[0] != n or self.parent.device != device:
+            raise ValueError("the tree must have an entry for each new token, on the batch's "
+                             "device")
+
+
 class PagedWorkspace:
     """Scratch memory and status word of the paged calls on this batch with
-    n_tokens rows of new tokens (default: one for each sequence).  Calls with
-    other sizes, fewer tokens among them, may need more and then raise
-    ERR_CAPACITY.  One call at a time: calls that may run at once (on two
-    streams, or in two captured graphs) need a workspace each."""
+    n_tokens rows of new tokens (default: one for each sequence), and of
+    attend_tree_async if a tree is given.  Calls with other sizes, fewer
+    tokens among them, may need more and then raise ERR_CAPACITY.  One call at
+    a time: calls that may run at once (on two streams, or in two captured
+    graphs) need a workspace each."""
 
-    def __init__(self, desc: PagedDesc, batch: PagedBatch, n_tokens: Optional[int] = None):
+    def __init__(self, desc: PagedDesc, batch: PagedBatch, n_tokens: Optional[int] = None,
+                 tree: Optional[Tree] = None):
         b = batch._args(desc, batch.n_seqs if n_tokens is None else n_tokens)
         self.ws_bytes = int(lib().kvc_attend_ws_bytes(ctypes.byref(desc), ctypes.byref(b)))
+        if tree is not None:
+            self.ws_bytes = max(self.ws_bytes, int(lib().kvc_attend_tree_ws_bytes(
+                ctypes.byref(desc), ctypes.byref(b), tree._args())))
         self.ws = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=batch.device)
         self.status = _dev_status(batch.device)
 
@@ -909,6 +999,25 @@ class Rope:
     def _args(self) -> _RopeArgs:
         t = self.cos_sin
         return _RopeArgs(t.data_ptr(), t.shape[0], t.shape[1], int(self.interleaved), 0)
+
+
+class HeadNorm:
+    """kvc_head_norm: x w / sqrt(mean(x^2) + eps) over each head, with float32
+    weights [head_dim] for queries and for keys (a model's 16-bit weights are
+    converted once; where it multiplies by 1 + w, they hold that)."""
+
+    def __init__(self, q_weight: torch.Tensor, k_weight: torch.Tensor, eps: float = 1e-6):
+        for w in (q_weight, k_weight):
+            if (not w.is_cuda or w.dtype != torch.float32 or w.dim() != 1
+                    or not w.is_contiguous()):
+                raise ValueError("the norms' weights must be contiguous [head_dim] float32 CUDA "
+                                 "tensors")
+        if q_weight.shape != k_weight.shape or q_weight.device != k_weight.device:
+            raise ValueError("the norms' weights must have one shape and device")
+        self.q_weight, self.k_weight, self.eps = q_weight, k_weight, float(eps)
+
+    def _args(self) -> _HeadNormArgs:
+        return _HeadNormArgs(self.q_weight.data_ptr(), self.k_weight.data_ptr(), self.eps, 0)
 
 
 def _cache_type(desc: PagedDesc, t: torch.Tensor, what: str) -> None:
@@ -956,10 +1065,13 @@ def _paged_stream(stream: Optional[torch.cuda.Stream], device):
 def append_async(desc: PagedDesc, batch: PagedBatch, layer: int, pool: torch.Tensor,
                  k: torch.Tensor, v: torch.Tensor, wsp: PagedWorkspace,
                  rope: Optional[Rope] = None, q: Optional[torch.Tensor] = None,
-                 q_out: Optional[torch.Tensor] = None, stream=None) -> None:
+                 q_out: Optional[torch.Tensor] = None, stream=None,
+                 norm: Optional[HeadNorm] = None, tree: Optional[Tree] = None) -> None:
     """Launch kvc_append: the batch's new tokens k, v [n_tokens][n_kv_heads]
     [head_dim] into their slots of `layer`, keys (and queries q into q_out)
-    turned by rope (no sync; device errors stay in wsp.status)."""
+    turned by rope (no sync; device errors stay in wsp.status).  With norm or
+    tree, kvc_append_norm: keys and queries are normed head by head first, and
+    a tree's tokens are turned to their depths' positions."""
     dev = batch.device
     n = k.shape[0]
     heads, dim, dtype = desc.n_kv_heads, desc.head_dim, _DTYPES[desc.io_dtype]
@@ -976,16 +1088,39 @@ def append_async(desc: PagedDesc, batch: PagedBatch, layer: int, pool: torch.Ten
     if rope is not None and rope.cos_sin.device != dev:
         raise ValueError("the rotation table must be on the batch's device")
     _workspace_check(wsp, dev)
-    _check(lib().kvc_append(desc, batch._args(desc, n), layer, _pool_ptr(desc, pool, dev),
-                            k.data_ptr(), ks, v.data_ptr(), vs,
-                            None if q is None else q.data_ptr(), qs,
-                            None if q is None else q_out.data_ptr(), os_,
-                            None if rope is None else rope._args(), wsp.status.data_ptr(),
-                            _paged_stream(stream, dev)), "kvc_append")
+    args = (desc, batch._args(desc, n), layer, _pool_ptr(desc, pool, dev), k.data_ptr(), ks,
+            v.data_ptr(), vs, None if q is None else q.data_ptr(), qs,
+            None if q is None else q_out.data_ptr(), os_, None if rope is None else rope._args())
+    if norm is None and tree is None:
+        _check(lib().kvc_append(*args, wsp.status.data_ptr(), _paged_stream(stream, dev)),
+               "kvc_append")
+        return
+    if norm is not None and (norm.k_weight.shape[0] != dim or norm.k_weight.device != dev):
+        raise ValueError("the norms' weights must have head_dim entries, on the batch's device")
+    if tree is not None:
+        tree._check(n, dev)
+        if batch.q_start is None:
+            raise ValueError("a tree needs a batch with q_start")
+    _check(lib().kvc_append_norm(*args, None if norm is None else norm._args(),
+                                 None if tree is None else tree.depth.data_ptr(),
+                                 wsp.status.data_ptr(), _paged_stream(stream, dev)),
+           "kvc_append_norm")
+
+
+def tree_async(desc: PagedDesc, batch: PagedBatch, tree: Tree, wsp: PagedWorkspace,
+               stream=None) -> None:
+    """Launch kvc_tree_build: the tree's mask and depth from its parents (no
+    sync; device errors stay in wsp.status)."""
+    dev = batch.device
+    n = tree.parent.shape[0]
+    tree._check(n, dev)
+    _workspace_check(wsp, dev)
+    _check(lib().kvc_tree_build(desc, batch._args(desc, n), tree._args(), wsp.status.data_ptr(),
+                                _paged_stream(stream, dev)), "kvc_tree_build")
 
 
 def _attend(name: str, desc: PagedDesc, batch: PagedBatch, layer: int, pool, q, out, wsp, scale,
-            window, lse, stream) -> None:
+            window, lse, stream, sinks: int = 0, tree: Optional[Tree] = None) -> None:
     dev = batch.device
     n = q.shape[0]
     heads, dim, dtype = desc.n_heads, desc.head_dim, _DTYPES[desc.io_dtype]
@@ -995,32 +1130,141 @@ def _attend(name: str, desc: PagedDesc, batch: PagedBatch, layer: int, pool, q, 
                             or lse.dtype != torch.float32 or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous [n_tokens][n_heads] float32 tensor")
     _u32(window, "window")
+    _u32(sinks, "sinks")
     _u32(layer, "layer")
     _workspace_check(wsp, dev)
-    _check(getattr(lib(), name)(desc, batch._args(desc, n), layer, _pool_ptr(desc, pool, dev),
-                                q.data_ptr(), qs, dim ** -0.5 if scale is None else scale, window,
-                                out.data_ptr(), os_, None if lse is None else lse.data_ptr(),
-                                wsp.ws.data_ptr(), wsp.ws_bytes, wsp.status.data_ptr(),
-                                _paged_stream(stream, dev)), name)
+    head = (layer, _pool_ptr(desc, pool, dev), q.data_ptr(), qs,
+            dim ** -0.5 if scale is None else scale)
+    tail = (out.data_ptr(), os_, None if lse is None else lse.data_ptr(), wsp.ws.data_ptr(),
+            wsp.ws_bytes, wsp.status.data_ptr(), _paged_stream(stream, dev))
+    if tree is not None:
+        tree._check(n, dev)
+        code = lib().kvc_attend_tree(desc, batch._args(desc, n), tree._args(), *head, *tail)
+    elif sinks:
+        if (name == "kvc_attend") != (batch.q_start is None):
+            raise KvcError(ERR_INVALID_ARG, name)
+        code = lib().kvc_attend_sinks(desc, batch._args(desc, n), *head, window, sinks, *tail)
+    else:
+        code = getattr(lib(), name)(desc, batch._args(desc, n), *head, window, *tail)
+    _check(code, name)
 
 
 def attend_async(desc: PagedDesc, batch: PagedBatch, layer: int, pool: torch.Tensor,
                  q: torch.Tensor, out: torch.Tensor, wsp: PagedWorkspace,
                  scale: Optional[float] = None, window: int = 0,
-                 lse: Optional[torch.Tensor] = None, stream=None) -> None:
+                 lse: Optional[torch.Tensor] = None, stream=None, sinks: int = 0) -> None:
     """Launch kvc_attend: each sequence's one new token q [n_seqs][n_heads]
     [head_dim] over its cache, into out (and the log-sum-exp into lse
-    [n_seqs][n_heads]).  scale defaults to head_dim^-1/2 (no sync)."""
-    _attend("kvc_attend", desc, batch, layer, pool, q, out, wsp, scale, window, lse, stream)
+    [n_seqs][n_heads]).  scale defaults to head_dim^-1/2.  With a window, the
+    sequence's first `sinks` tokens stay visible behind it (no sync)."""
+    _attend("kvc_attend", desc, batch, layer, pool, q, out, wsp, scale, window, lse, stream, sinks)
 
 
 def attend_prompt_async(desc: PagedDesc, batch: PagedBatch, layer: int, pool: torch.Tensor,
                         q: torch.Tensor, out: torch.Tensor, wsp: PagedWorkspace,
                         scale: Optional[float] = None, window: int = 0,
-                        lse: Optional[torch.Tensor] = None, stream=None) -> None:
+                        lse: Optional[torch.Tensor] = None, stream=None,
+                        sinks: int = 0) -> None:
     """Launch kvc_attend_prompt: several new tokens a sequence (batch.q_start),
-    each over the tokens up to its own position (no sync)."""
-    _attend("kvc_attend_prompt", desc, batch, layer, pool, q, out, wsp, scale, window, lse, stream)
+    each over the tokens up to its own position; window and sinks as for
+    attend_async (no sync)."""
+    _attend("kvc_attend_prompt", desc, batch, layer, pool, q, out, wsp, scale, window, lse, stream,
+            sinks)
+
+
+def attend_tree_async(desc: PagedDesc, batch: PagedBatch, tree: Tree, layer: int,
+                      pool: torch.Tensor, q: torch.Tensor, out: torch.Tensor, wsp: PagedWorkspace,
+                      scale: Optional[float] = None, lse: Optional[torch.Tensor] = None,
+                      stream=None) -> None:
+    """Launch kvc_attend_tree: a tree's tokens (batch.q_start), each over the
+    cached context and the tree's tokens on its path (no sync).  wsp must have
+    been made with the tree."""
+    _attend("kvc_attend_tree", desc, batch, layer, pool, q, out, wsp, scale, 0, lse, stream,
+            tree=tree)
+
+
+def keep_async(desc: PagedDesc, batch: PagedBatch, pool: torch.Tensor, path: torch.Tensor,
+               kept: torch.Tensor, new_lens: torch.Tensor, n_tokens: int, status: torch.Tensor,
+               stream=None) -> None:
+    """Launch kvc_keep: of the batch's n_tokens new tokens, each sequence's
+    path[b][:kept[b]] (rising numbers among its own) move to the front, in
+    every layer, and new_lens[b] is the length with them alone (no sync;
+    device errors stay in status).  path [n_seqs][entries], kept and new_lens
+    [n_seqs] are int32; new_lens is not batch.lens."""
+    dev = batch.device
+    _u32(n_tokens, "n_tokens")
+    _int32_tensor(path, 2, "path")
+    for t, what in ((kept, "kept"), (new_lens, "new_lens"), (status, "status")):
+        _int32_tensor(t, 1, what)
+        if t.device != dev:
+            raise ValueError(f"{what} must be on the batch's device")
+    n = batch.n_seqs
+    if path.device != dev or path.shape[0] != n or kept.shape[0] != n or new_lens.shape[0] != n:
+        raise ValueError("path, kept and new_lens must have a row for each sequence, on the "
+                         "batch's device")
+    _check(lib().kvc_keep(desc, batch._args(desc, n_tokens), _pool_ptr(desc, pool, dev),
+                          path.data_ptr(), path.shape[1], kept.data_ptr(), new_lens.data_ptr(),
+                          status.data_ptr(), _paged_stream(stream, dev)), "kvc_keep")
+
+
+class PageLedger:
+    """kvc_ledger: which pages the rows of table [rows][entries] hold, with
+    lens [rows] tokens each, and how many rows hold each page: refs [n_pages]
+    (default: no page is held, all lens are 0).  table and lens may be a
+    PagedBatch's.  fork_async and resize_async keep the three in line; device
+    errors stay in status.  One call at a time: the ledger has their workspace."""
+
+    def __init__(self, desc: PagedDesc, table: torch.Tensor, lens: torch.Tensor,
+                 refs: Optional[torch.Tensor] = None):
+        dev = table.device
+        self.desc, self.device = desc, dev
+        self.table = _int32_tensor(table, 2, "table")
+        self.lens = _int32_tensor(lens, 1, "lens")
+        if refs is None:
+            refs = torch.zeros(desc.n_pages, dtype=torch.int32, device=dev)
+        self.refs = _int32_tensor(refs, 1, "refs")
+        if lens.shape[0] != table.shape[0] or refs.shape[0] != desc.n_pages:
+            raise ValueError("lens must have an entry for each row, refs one for each page")
+        if lens.device != dev or refs.device != dev:
+            raise ValueError("the ledger's tensors must be on one device")
+        self.ws_bytes = int(lib().kvc_resize_ws_bytes(ctypes.byref(desc)))
+        self.ws = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=dev)
+        self.status = _dev_status(dev)
+
+    def _args(self) -> _LedgerArgs:
+        return _LedgerArgs(self.table.data_ptr(), self.lens.data_ptr(), self.refs.data_ptr(),
+                           self.table.shape[0], self.table.shape[1])
+
+    def _rows(self, t: torch.Tensor, what: str) -> int:
+        if _int32_tensor(t, 1, what).device != self.device:
+            raise ValueError(f"{what} must be on the ledger's device")
+        return t.data_ptr()
+
+
+def fork_async(ledger: PageLedger, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
+    """Launch kvc_fork: rows dst give up their pages and share those of rows
+    src (int32; a negative src leaves its fork out).  No token is copied before
+    a row grows (no sync)."""
+    s, d = ledger._rows(src, "src"), ledger._rows(dst, "dst")
+    if src.shape != dst.shape:
+        raise ValueError("src and dst must have the same length")
+    _check(lib().kvc_fork(ledger.desc, ledger._args(), s, d, src.shape[0],
+                          ledger.status.data_ptr(), _paged_stream(stream, ledger.device)),
+           "kvc_fork")
+
+
+def resize_async(ledger: PageLedger, pool: torch.Tensor, new_lens: torch.Tensor,
+                 stream=None) -> None:
+    """Launch kvc_resize: every row shrinks or grows to new_lens [rows] tokens
+    (0 frees it).  A row that grows out of a page that others hold too gets a
+    copy of its own (no sync)."""
+    n = ledger._rows(new_lens, "new_lens")
+    if new_lens.shape != ledger.lens.shape:
+        raise ValueError("new_lens must have an entry for each row")
+    _check(lib().kvc_resize(ledger.desc, ledger._args(), n,
+                            _pool_ptr(ledger.desc, pool, ledger.device), ledger.ws.data_ptr(),
+                            ledger.ws_bytes, ledger.status.data_ptr(),
+                            _paged_stream(stream, ledger.device)), "kvc_resize")
 
 
 def _page_args(desc: PagedDesc, pool, table, flat, status, *tokens):

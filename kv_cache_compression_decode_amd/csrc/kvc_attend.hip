@@ -142,6 +142,13 @@ __device__ inline bool nonfinite2(uint32_t w) {
   return (w & e) == e || (w & (e << 16)) == (e << 16);
 }
 
+// A row's visible tokens are counted in one run, sinks included: the s sinks
+// that its window, from token lo on, does not reach stand for the tokens
+// [lo - s, lo), so that only a token's lookup knows of the gap between them.
+__device__ inline int32_t token_of(int32_t j, int32_t lo, int32_t first) {
+  return j < lo ? j - first : j;
+}
+
 // ---------------------------------------------------- sharing out the tokens
 // One new token a sequence, up to 16 query heads to a KV head: the work of a
 // call is a line of steps (a tile of 32 tokens of one KV head; more tiles where
@@ -179,9 +186,15 @@ struct Work {
     const int32_t n = len - first_of(a, len);
     return (n > 0 ? ((uint32_t)n - 1) >> a.step_shift : 0) + 1;
   }
-  // the first visible token
-  __device__ static int32_t first_of(const AttendArgs &a, int32_t len) {
+  // the window's first token
+  __device__ static int32_t window_of(const AttendArgs &a, int32_t len) {
     return a.window != 0 && (uint32_t)len > a.window ? len - (int32_t)a.window : 0;
+  }
+  // The visible tokens are [first_of, len), the sinks counted as the tokens
+  // next before the window (token_of).
+  __device__ static int32_t first_of(const AttendArgs &a, int32_t len) {
+    const int32_t lo = window_of(a, len);
+    return lo - (int32_t)min((uint32_t)lo, a.sinks);
   }
   __device__ void load(const AttendArgs &a, uint32_t seq) {
     b = seq;
@@ -358,6 +371,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
     const uint32_t first = row_tile * kRowTile, rows = min(kRowTile, a.group - first);
     const bool live = n16 < rows;
     const int32_t begin = Work::first_of(a, u.len), end = u.len;
+    const int32_t lo = Work::window_of(a, u.len);
     const int32_t tiles = end > begin ? (int32_t)(((uint32_t)(end - begin) + kTok - 1) / kTok) : 0;
     // a step is 2^(step_shift - 5) tiles
     const uint32_t per_step = a.step_shift - 5;
@@ -377,7 +391,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_rows(AttendArg
     uint32_t next_id = 0, next_in = 0;  // page id; token within the page
     auto look_up = [&](int32_t ti) {
       int32_t j = begin + ti * (int32_t)kTok + (int32_t)(lane & 31);
-      j = j < last ? j : last;
+      j = token_of(j < last ? j : last, lo, begin);
       const uint32_t page = a.s.page.div((uint32_t)j);
       next_id = (uint32_t)table[page];
       next_in = (uint32_t)j - page * a.s.page.d;
@@ -735,20 +749,44 @@ struct Tile {
   uint32_t first, rows;
 };
 
-// Where a row writes, and its visible tokens [lo, hi).
+// Where a row writes, and its visible tokens: [lo, hi) and the sinks; in a
+// tree of new tokens those before `base` and those of them that its mask holds.
 struct Row {
   uint32_t token, head;  // row of q and out; head within the group
   int32_t lo, hi;
+  int32_t base, i;  // the sequence's first new token; this row's among them
 };
 __device__ inline Row row_of(const AttendArgs &a, const Tile &t, int32_t len, uint32_t r) {
   Row w;
   const uint32_t i = a.group_div.div(r);
   w.head = r - i * a.group;
   w.token = t.row0 + i;
-  const int32_t pos = len - (int32_t)t.n + (int32_t)i;
+  w.base = len - (int32_t)t.n;
+  w.i = (int32_t)i;
+  const int32_t pos = w.base + w.i;
   w.hi = pos < 0 ? 0 : pos + 1;
   w.lo = a.window != 0 && (uint32_t)w.hi > a.window ? w.hi - (int32_t)a.window : 0;
   return w;
+}
+
+// Which of the 64 tokens from j0 on a row of a tree sees; needs j0 + 64 >
+// base (all before are seen).  A row sees itself whatever its mask says, and
+// nothing behind itself.
+__device__ inline uint64_t tree_sees(const AttendArgs &a, const Row &row, int32_t j0) {
+  const uint64_t *mask = a.mask + (uint64_t)row.token * a.mask_words;
+  const auto word = [&](uint32_t k) { return k < a.mask_words ? mask[k] : 0ull; };
+  const int32_t t0 = j0 - row.base;
+  uint64_t see;
+  if (t0 < 0) {
+    see = word(0) << -t0 | ((1ull << -t0) - 1);
+  } else {
+    const uint32_t k = (uint32_t)t0 >> 6, sh = (uint32_t)t0 & 63;
+    see = word(k) >> sh;
+    if (sh) see |= word(k + 1) << (64 - sh);
+  }
+  const int32_t self = row.i - t0, n = row.hi - j0;
+  if (self >= 0 && self < 64) see |= 1ull << self;
+  return n <= 0 ? 0 : n < 64 ? see & ((1ull << n) - 1) : see;
 }
 
 // Row tile `t` of the call: the sequences in order, of each its last tile (the
@@ -791,7 +829,7 @@ __device__ inline bool find_tile(const AttendArgs &a, uint32_t t, Tile &out) {
   return false;
 }
 
-template <class TI, class TC, int D, int NW>
+template <class TI, class TC, int D, int NW, bool kTree>
 __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tile(AttendArgs a) {
   constexpr int TOK = kBigTok<D>, HT = TOK / 32;
   constexpr uint32_t kThreads = NW * 64, kRows = NW * 32;
@@ -810,7 +848,10 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tile(
   const uint32_t rest = blockIdx.x / a.n_kv_heads;
   const uint32_t split = rest % a.splits, tile = rest / a.splits;
   Tile t;
-  if (blockIdx.x == 0) a.s.check(a.status);
+  if (blockIdx.x == 0) {
+    a.s.check(a.status);
+    if (kTree) a.s.check_new(a.max_new, a.status);
+  }
   if (!find_tile<kRows>(a, tile, t)) return;
   const int32_t len = a.s.len(t.b);
   const uint32_t w0 = wave * 32;
@@ -820,7 +861,13 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tile(
   const Row r_first = row_of(a, t, len, t.first), r_last = row_of(a, t, len, t.first + t.rows - 1);
   const Row w_first = row_of(a, t, len, t.first + (busy ? w0 : 0));
   const Row w_last = row_of(a, t, len, t.first + (busy ? min(w0 + 31, t.rows - 1) : 0));
-  const int32_t begin = r_first.lo, end = r_last.hi, last = end - 1;
+  // r_first's window is the first to begin; the sinks before it (token_of)
+  const int32_t lo = r_first.lo, begin = lo - (int32_t)min((uint32_t)lo, a.sinks);
+  const int32_t sink_end = a.sinks ? max(lo, (int32_t)a.sinks) : begin;  // tokens below: sinks
+  const int32_t end = r_last.hi, last = end - 1;
+  // tokens below are seen by every row of the workgroup, of the wave
+  const int32_t r_full = kTree ? r_first.base : r_first.hi;
+  const int32_t w_full = kTree ? r_first.base : w_first.hi;
   const int32_t n_tiles = end > begin ? (end - begin + TOK - 1) / TOK : 0;
   const int32_t t_lo = (int32_t)((int64_t)n_tiles * split / a.splits);
   const int32_t t_hi = (int32_t)((int64_t)n_tiles * (split + 1) / a.splits);
@@ -857,7 +904,7 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tile(
   uint32_t next_id = 0, next_in = 0;  // page id; token within the page
   auto look_up = [&](int32_t ti) {
     int32_t j = begin + ti * TOK + (int32_t)my_t;
-    j = j < last ? j : last;
+    j = token_of(j < last ? j : last, lo, begin);
     const uint32_t page = a.s.page.div((uint32_t)j);
     next_id = (uint32_t)table[page];
     next_in = (uint32_t)j - page * a.s.page.d;
@@ -882,7 +929,7 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tile(
     const int32_t j0 = begin + ti * TOK;
     uint8_t *kb = lds + (ti & 1) * kKeyBuf<D>;
     uint8_t *vb = s_val + (VB == 3 ? odd_at : ti & 1) * kValBuf<D>;
-    if (j0 < r_last.lo || j0 + TOK > r_first.hi) {
+    if (j0 < r_last.lo || j0 + TOK > r_full) {
       bool nf = false;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
@@ -951,7 +998,7 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tile(
     uint64_t odd = 0;
     // the slot that tile ti + 2 will use: last read a barrier ago
     if (threadIdx.x < 2) s_odd[next_odd_of(next_odd) * 2 + threadIdx.x] = 0;
-    if (j0 < r_last.lo || j0 + TOK > r_first.hi) {
+    if (j0 < r_last.lo || j0 + TOK > r_full) {
       odd = s_odd[odd_at * 2] | (uint64_t)s_odd[odd_at * 2 + 1] << 32;
       if (odd) {
         __syncthreads();  // every wave has read the mask
@@ -966,7 +1013,7 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tile(
       pending = false;
     }
     // a wave has nothing to do where none of its rows sees a token
-    if (busy && j0 < w_last.hi && j0 + TOK > w_first.lo) {
+    if (busy && j0 < w_last.hi && (j0 + TOK > w_first.lo || j0 < sink_end)) {
       // the matrix unit's feeder goes first where another wave has vector work
       __builtin_amdgcn_s_setprio(1);
       f32x16 s[HT];
@@ -992,14 +1039,25 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tile(
         }
         __builtin_amdgcn_sched_group_barrier(0x8, depth, 0);
       }
-      if (j0 < w_last.lo || j0 + TOK > w_first.hi) {
+      uint64_t see = 0;
+      if (j0 < w_last.lo || j0 + TOK > w_full) {
+        if constexpr (kTree) {
+          see = tree_sees(a, row, j0);
+          const uint64_t mine = see >> (hi * 4);
 #pragma unroll
-        for (int h = 0; h < HT; ++h)
+          for (int h = 0; h < HT; ++h)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int32_t j = j0 + h * 32 + (i >> 2) * 8 + (int32_t)hi * 4 + (i & 3);
-            s[h][i] = j >= row.lo && j < row.hi ? s[h][i] : ninf();
-          }
+            for (int i = 0; i < 16; ++i)
+              s[h][i] = (mine >> (h * 32 + (i >> 2) * 8 + (i & 3))) & 1 ? s[h][i] : ninf();
+        } else {
+#pragma unroll
+          for (int h = 0; h < HT; ++h)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int32_t j = j0 + h * 32 + (i >> 2) * 8 + (int32_t)hi * 4 + (i & 3);
+              s[h][i] = (j >= row.lo || j < sink_end) && j < row.hi ? s[h][i] : ninf();
+            }
+        }
       }
       __builtin_amdgcn_s_setprio(0);
       float mt = s[0][0];
@@ -1034,8 +1092,8 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tile(
         pj = __shfl(pj, (int)(n32 + 32 * ((e >> 2) & 1)));
         const int32_t j = j0 + (int32_t)jt;
         uint32_t sj;
-        a.s.slot_of(table, (uint32_t)(j < last ? j : last), sj);
-        if (j >= row.lo && j < row.hi) {
+        a.s.slot_of(table, (uint32_t)token_of(j < last ? j : last, lo, begin), sj);
+        if (kTree ? (see >> jt) & 1 : (j >= row.lo || j < sink_end) && j < row.hi) {
           const TC *vp = vbase + (uint64_t)sj * a.row + hi * 4;
 #pragma unroll
           for (int d = 0; d < DT; ++d)
@@ -1166,7 +1224,7 @@ constexpr uint32_t kWholeSteps = 16;
 // A 16-row workgroup takes at least a step for each wave of a head.
 uint32_t min_steps(const Plan &w) { return 4 / w.wg_heads; }
 
-Plan make_plan(const kvc_paged_desc &p, const kvc_paged_batch &b) {
+Plan make_plan(const kvc_paged_desc &p, const kvc_paged_batch &b, uint32_t max_new) {
   Plan w{};
   if (b.n_seqs == 0 || b.n_tokens == 0) return w;
   const uint32_t group = p.n_heads / p.n_kv_heads;
@@ -1230,10 +1288,10 @@ Plan make_plan(const kvc_paged_desc &p, const kvc_paged_batch &b) {
   return w;
 }
 
-template <class TI, class TC, int D>
+template <class TI, class TC, int D, bool kTree>
 hipError_t launch_d(const AttendArgs &a, const Plan &w, hipStream_t stream) {
   const uint32_t units = w.tiles * a.n_kv_heads;
-  if (w.rows == 16) {
+  if constexpr (!kTree) if (w.rows == 16) {
     hipLaunchKernelGGL((k_attend_rows<TI, TC, D>), dim3(w.grid), dim3(256), 0, stream, a);
     if (w.join) {
       const dim3 grid((uint32_t)w.infos, std::min(kRowTile, a.group), w.wg_heads);
@@ -1242,45 +1300,50 @@ hipError_t launch_d(const AttendArgs &a, const Plan &w, hipStream_t stream) {
       else
         hipLaunchKernelGGL((k_attend_rows_join<TI, TC, D, 4>), grid, dim3(256), 0, stream, a);
     }
-  } else {
-    const auto tile = [&](auto nw) {
-      constexpr int NW = decltype(nw)::value;
-      hipLaunchKernelGGL((k_attend_tile<TI, TC, D, NW>), dim3(units * w.splits), dim3(NW * 64),
-                         (kBigLds<D, NW>), stream, a);
-      if (w.join)
-        hipLaunchKernelGGL((k_attend_tile_join<TI, TC, D, NW * 32>), dim3(units * (NW * 8)),
-                           dim3(256), 0, stream, a);
-    };
-    if constexpr (D != 256)
-      if (w.rows == 256) {
-        tile(std::integral_constant<int, 8>{});
-        return hipGetLastError();
-      }
-    tile(std::integral_constant<int, 4>{});
+    return hipGetLastError();
   }
+  const auto tile = [&](auto nw) {
+    constexpr int NW = decltype(nw)::value;
+    hipLaunchKernelGGL((k_attend_tile<TI, TC, D, NW, kTree>), dim3(units * w.splits),
+                       dim3(NW * 64), (kBigLds<D, NW>), stream, a);
+    if (w.join)
+      hipLaunchKernelGGL((k_attend_tile_join<TI, TC, D, NW * 32>), dim3(units * (NW * 8)),
+                         dim3(256), 0, stream, a);
+  };
+  if constexpr (D != 256)
+    if (w.rows == 256) {
+      tile(std::integral_constant<int, 8>{});
+      return hipGetLastError();
+    }
+  tile(std::integral_constant<int, 4>{});
   return hipGetLastError();
 }
 
+template <class TI, class TC, bool kTree>
+hipError_t launch_m(const kvc_paged_desc &p, const AttendArgs &a, const Plan &w,
+                    hipStream_t stream) {
+  switch (p.head_dim) {
+    case 64: return launch_d<TI, TC, 64, kTree>(a, w, stream);
+    case 96: return launch_d<TI, TC, 96, kTree>(a, w, stream);
+    case 128: return launch_d<TI, TC, 128, kTree>(a, w, stream);
+    default: return launch_d<TI, TC, 256, kTree>(a, w, stream);
+  }
+}
 template <class TI, class TC>
 hipError_t launch_t(const kvc_paged_desc &p, const AttendArgs &a, const Plan &w,
                     hipStream_t stream) {
-  switch (p.head_dim) {
-    case 64: return launch_d<TI, TC, 64>(a, w, stream);
-    case 96: return launch_d<TI, TC, 96>(a, w, stream);
-    case 128: return launch_d<TI, TC, 128>(a, w, stream);
-    default: return launch_d<TI, TC, 256>(a, w, stream);
-  }
+  return a.mask ? launch_m<TI, TC, true>(p, a, w, stream) : launch_m<TI, TC, false>(p, a, w, stream);
 }
 
 }  // namespace
 
-uint64_t attend_ws_bytes(const kvc_paged_desc &p, const kvc_paged_batch &b) {
-  return make_plan(p, b).total;
+uint64_t attend_ws_bytes(const kvc_paged_desc &p, const kvc_paged_batch &b, uint32_t max_new) {
+  return make_plan(p, b, max_new).total;
 }
 
 hipError_t launch_attend(const kvc_paged_desc &p, const kvc_paged_batch &b, AttendArgs a, void *ws,
                          hipStream_t stream) {
-  const Plan w = make_plan(p, b);
+  const Plan w = make_plan(p, b, a.max_new);
   a.splits = w.splits;
   a.whole = w.whole;
   a.seq_tiles = (a.group + kRowTile - 1) / kRowTile;

@@ -116,6 +116,16 @@ struct Seqs {
       bad = bad || rows_bad(b) || len_bad(b);
     if (bad) set_status(status, KVC_ERR_SHAPE);
   }
+  // ... and a sequence with more than `most` new tokens
+  __device__ inline void check_new(uint32_t most, int32_t *status) const {
+    bool bad = false;
+    for (uint32_t b = threadIdx.x; b < n_seqs; b += blockDim.x) {
+      uint32_t row, n;
+      rows(b, row, n);
+      bad = bad || n > most;
+    }
+    if (bad) set_status(status, KVC_ERR_SHAPE);
+  }
   // Slot (token row of the pool) of token `in` of page `id`.  False for an id
   // outside the pool; the slot is then one inside it, so that a caller that
   // goes on reads nothing out of bounds.
@@ -130,6 +140,82 @@ struct Seqs {
     return slot_in((uint32_t)ids[e], j - e * page.d, slot);
   }
 };
+
+// 8 elements as binary32 and back.
+template <class T>
+__device__ inline void widen8(u32x4 w, float *x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = elem_lo<T>(w[i]);
+    x[2 * i + 1] = elem_hi<T>(w[i]);
+  }
+}
+template <class T>
+__device__ inline u32x4 narrow8(const float *x) {
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = pack2<T>(x[2 * i], x[2 * i + 1]);
+  return w;
+}
+
+// A vector without rotation: its bits if the types agree (NaN payloads kept).
+template <class TI, class TO>
+__device__ inline u32x4 convert8(u32x4 w) {
+  if constexpr (std::is_same<TI, TO>::value) {
+    return w;
+  } else {
+    float x[8];
+    widen8<TI>(w, x);
+    return narrow8<TO>(x);
+  }
+}
+
+// 4 pairs (2j, 2j + 1) in a vector, with their 4 cosines and sines.
+template <class TI, class TO>
+__device__ inline u32x4 turn_inter(u32x4 w, const float *c, const float *s) {
+  float x[8], y[8];
+  widen8<TI>(w, x);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    y[2 * i] = __builtin_fmaf(x[2 * i], c[i], -(x[2 * i + 1] * s[i]));
+    y[2 * i + 1] = __builtin_fmaf(x[2 * i + 1], c[i], x[2 * i] * s[i]);
+  }
+  return narrow8<TO>(y);
+}
+
+// The last sequence whose first row is at most `row` (q_start[0] <= row).
+__device__ inline uint32_t seq_of_row(const Seqs &s, uint32_t row) {
+  uint32_t lo = 0, hi = s.n_seqs;
+  while (hi - lo > 1) {
+    const uint32_t mid = (lo + hi) / 2;
+    if (s.q_start[mid] <= (int32_t)row)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// Argument checks shared by the paged calls (kvc_paged.hip).
+inline bool aligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+bool paged_ok(const kvc_paged_desc *p);
+// the batch's sizes (not its pointers)
+kvc_status batch_sizes(const kvc_paged_desc *p, const kvc_paged_batch *b);
+// ... and its pointers, the layer, the pool and the status word
+kvc_status batch_check(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t layer,
+                       const void *pool, const int32_t *dev_status);
+// rows [n][heads][head_dim] `stride` elements apart
+kvc_status rows_check(const void *p, uint64_t stride, uint32_t n, uint64_t width);
+kvc_status rope_check(const kvc_paged_desc *p, const kvc_rope *rope);
+// everything that kvc_append and kvc_append_norm share
+kvc_status append_check(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t layer,
+                        const void *pool, const void *k, uint64_t k_stride, const void *v,
+                        uint64_t v_stride, const void *q, uint64_t q_stride, const void *q_out,
+                        uint64_t q_out_stride, const kvc_rope *rope, const int32_t *dev_status);
+constexpr uint32_t kTreeTokens = 4096;  // of a sequence's tree at most
+bool tree_ok(const kvc_tree *t);        // its sizes, not its pointers
+Seqs to_seqs(const kvc_paged_desc *p, const kvc_paged_batch *b);
+uint64_t plane_bytes(const kvc_paged_desc *p);  // a layer's keys (or values)
 
 hipError_t launch_append(const kvc_paged_desc &p, const Seqs &s, uint32_t layer, void *pool,
                          const void *k, uint64_t k_stride, const void *v, uint64_t v_stride,
@@ -165,10 +251,13 @@ struct AttendArgs {
   bool by_unit;        // the layout of its join records
   bool whole;          // the 16-row kernel takes sequences as a whole
   float scale;      // scale * log2(e)
-  uint32_t window;
+  uint32_t window, sinks;  // sinks: 0 without a window
+  const uint64_t *mask;    // a tree's [n_tokens][mask_words], or nullptr
+  uint32_t mask_words, max_new;
   int32_t *status;
 };
-uint64_t attend_ws_bytes(const kvc_paged_desc &p, const kvc_paged_batch &b);
+// max_new: a tree's bound of the new tokens of a sequence, 0 without a tree
+uint64_t attend_ws_bytes(const kvc_paged_desc &p, const kvc_paged_batch &b, uint32_t max_new);
 hipError_t launch_attend(const kvc_paged_desc &p, const kvc_paged_batch &b, AttendArgs a, void *ws,
                          hipStream_t stream);
 

@@ -1,8 +1,105 @@
 // The paged KV cache's entry points (argument checks), appending new tokens
 // with their rotation, and moving a context between pages and a tensor.
+#include <algorithm>
+
 #include "kvc_paged.h"
 
 namespace kvc {
+
+// ---------------------------------------------------------- argument checks
+bool paged_ok(const kvc_paged_desc *p) {
+  if (!p) return false;
+  if (p->n_layers < 1 || p->n_kv_heads < 1 || p->n_heads < 1) return false;
+  if (p->n_heads % p->n_kv_heads != 0 || p->n_heads / p->n_kv_heads > 128) return false;
+  if (p->n_heads > 4096 || p->n_layers > 32767) return false;  // launch grids
+  if (p->head_dim != 64 && p->head_dim != 96 && p->head_dim != 128 && p->head_dim != 256)
+    return false;
+  if (p->page_tokens < 1 || p->n_pages < 1) return false;
+  if ((uint64_t)p->page_tokens * p->n_pages >= (1ull << 31)) return false;
+  if (p->cache_dtype > KVC_BF16 || p->io_dtype > KVC_BF16) return false;
+  return !(p->cache_dtype == KVC_BF16 && p->io_dtype == KVC_F16);
+}
+
+// The batch's sizes (not its pointers).
+kvc_status batch_sizes(const kvc_paged_desc *p, const kvc_paged_batch *b) {
+  if (!paged_ok(p) || !b) return KVC_ERR_INVALID_ARG;
+  // one block per row or row tile: launch grids below 2^32 threads
+  if (b->n_seqs > (1u << 20) || b->n_tokens > (1u << 20)) return KVC_ERR_SHAPE;
+  if (!b->q_start && b->n_tokens != b->n_seqs) return KVC_ERR_SHAPE;
+  if (b->max_len > (1u << 30)) return KVC_ERR_SHAPE;  // a tile's end stays in 31 bits
+  if (b->n_seqs && b->max_len > (uint64_t)b->table_stride * p->page_tokens) return KVC_ERR_SHAPE;
+  return KVC_OK;
+}
+
+kvc_status batch_check(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t layer,
+                       const void *pool, const int32_t *dev_status) {
+  const kvc_status st = batch_sizes(p, b);
+  if (st != KVC_OK) return st;
+  if (layer >= p->n_layers) return KVC_ERR_SHAPE;
+  if (!pool || !aligned(pool, 16) || !dev_status || !aligned(dev_status, 4))
+    return KVC_ERR_INVALID_ARG;
+  if (b->n_seqs && (!b->lens || !aligned(b->lens, 4))) return KVC_ERR_INVALID_ARG;
+  if (b->n_seqs && b->max_len && (!b->table || !aligned(b->table, 4))) return KVC_ERR_INVALID_ARG;
+  if (b->q_start && !aligned(b->q_start, 4)) return KVC_ERR_INVALID_ARG;
+  return KVC_OK;
+}
+
+// Rows [n][heads][head_dim] `stride` elements apart.
+kvc_status rows_check(const void *p, uint64_t stride, uint32_t n, uint64_t width) {
+  if (!p || !aligned(p, 16) || stride % 8 != 0) return KVC_ERR_INVALID_ARG;
+  if (n > 1 && stride < width) return KVC_ERR_SHAPE;
+  if (stride > (1ull << 40)) return KVC_ERR_SHAPE;
+  return KVC_OK;
+}
+
+kvc_status rope_check(const kvc_paged_desc *p, const kvc_rope *rope) {
+  if (!rope) return KVC_OK;
+  if (rope->reserved != 0 || rope->interleaved > 1) return KVC_ERR_INVALID_ARG;
+  if (rope->rotary_dim < 16 || rope->rotary_dim % 16 != 0 || rope->rotary_dim > p->head_dim)
+    return KVC_ERR_INVALID_ARG;
+  if (!rope->cos_sin || !aligned(rope->cos_sin, 16)) return KVC_ERR_INVALID_ARG;
+  return KVC_OK;
+}
+
+kvc_status append_check(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t layer,
+                        const void *pool, const void *k, uint64_t k_stride, const void *v,
+                        uint64_t v_stride, const void *q, uint64_t q_stride, const void *q_out,
+                        uint64_t q_out_stride, const kvc_rope *rope, const int32_t *dev_status) {
+  kvc_status st = batch_check(p, b, layer, pool, dev_status);
+  if (st != KVC_OK) return st;
+  if ((st = rope_check(p, rope)) != KVC_OK) return st;
+  if ((q == nullptr) != (q_out == nullptr)) return KVC_ERR_INVALID_ARG;
+  if (b->n_seqs == 0 || b->n_tokens == 0) return KVC_OK;
+  const uint64_t kw = (uint64_t)p->n_kv_heads * p->head_dim;
+  const uint64_t qw = (uint64_t)p->n_heads * p->head_dim;
+  if ((st = rows_check(k, k_stride, b->n_tokens, kw)) != KVC_OK) return st;
+  if ((st = rows_check(v, v_stride, b->n_tokens, kw)) != KVC_OK) return st;
+  if (q) {
+    if ((st = rows_check(q, q_stride, b->n_tokens, qw)) != KVC_OK) return st;
+    if ((st = rows_check(q_out, q_out_stride, b->n_tokens, qw)) != KVC_OK) return st;
+    if (q == q_out && q_stride != q_out_stride) return KVC_ERR_SHAPE;
+  }
+  return KVC_OK;
+}
+
+Seqs to_seqs(const kvc_paged_desc *p, const kvc_paged_batch *b) {
+  Seqs s;
+  s.table = b->table;
+  s.lens = b->lens;
+  s.q_start = b->q_start;
+  s.n_seqs = b->n_seqs;
+  s.table_stride = b->table_stride;
+  s.n_tokens = b->n_tokens;
+  s.max_len = b->max_len;
+  s.n_pages = p->n_pages;
+  s.page = FastDiv::make(p->page_tokens);
+  return s;
+}
+
+uint64_t plane_bytes(const kvc_paged_desc *p) {
+  return (uint64_t)p->n_pages * p->page_tokens * p->n_kv_heads * p->head_dim * 2;
+}
+
 namespace {
 
 // ------------------------------------------------------------------ append
@@ -35,48 +132,6 @@ struct AppendArgs {
   uint32_t n_positions;
   int32_t *status;
 };
-
-// 8 elements as binary32 and back.
-template <class T>
-__device__ inline void widen8(u32x4 w, float *x) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = elem_lo<T>(w[i]);
-    x[2 * i + 1] = elem_hi<T>(w[i]);
-  }
-}
-template <class T>
-__device__ inline u32x4 narrow8(const float *x) {
-  u32x4 w;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = pack2<T>(x[2 * i], x[2 * i + 1]);
-  return w;
-}
-
-// A vector without rotation: its bits if the types agree (NaN payloads kept).
-template <class TI, class TO>
-__device__ inline u32x4 convert8(u32x4 w) {
-  if constexpr (std::is_same<TI, TO>::value) {
-    return w;
-  } else {
-    float x[8];
-    widen8<TI>(w, x);
-    return narrow8<TO>(x);
-  }
-}
-
-// 4 pairs (2j, 2j + 1) in a vector, with their 4 cosines and sines.
-template <class TI, class TO>
-__device__ inline u32x4 turn_inter(u32x4 w, const float *c, const float *s) {
-  float x[8], y[8];
-  widen8<TI>(w, x);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    y[2 * i] = __builtin_fmaf(x[2 * i], c[i], -(x[2 * i + 1] * s[i]));
-    y[2 * i + 1] = __builtin_fmaf(x[2 * i + 1], c[i], x[2 * i] * s[i]);
-  }
-  return narrow8<TO>(y);
-}
 
 template <class TI, class TO, bool kStream>
 __device__ inline void append_item(const AppendArgs &a, const uint8_t *src, uint8_t *dst,
@@ -139,19 +194,6 @@ __device__ inline void append_item(const AppendArgs &a, const uint8_t *src, uint
     }
     move_store<kStream>(dst + (uint64_t)(base + d[i]) * 2, w[i]);
   }
-}
-
-// The last sequence whose first row is at most `row` (q_start[0] <= row).
-__device__ inline uint32_t seq_of_row(const Seqs &s, uint32_t row) {
-  uint32_t lo = 0, hi = s.n_seqs;
-  while (hi - lo > 1) {
-    const uint32_t mid = (lo + hi) / 2;
-    if (s.q_start[mid] <= (int32_t)row)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  return lo;
 }
 
 template <class TI, class TC, bool kStream>
@@ -245,71 +287,6 @@ __global__ __launch_bounds__(256) void k_page_copy(PageArgs a) {
   }
 }
 
-bool aligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
-
-bool paged_ok(const kvc_paged_desc *p) {
-  if (!p) return false;
-  if (p->n_layers < 1 || p->n_kv_heads < 1 || p->n_heads < 1) return false;
-  if (p->n_heads % p->n_kv_heads != 0 || p->n_heads / p->n_kv_heads > 128) return false;
-  if (p->n_heads > 4096 || p->n_layers > 32767) return false;  // launch grids
-  if (p->head_dim != 64 && p->head_dim != 96 && p->head_dim != 128 && p->head_dim != 256)
-    return false;
-  if (p->page_tokens < 1 || p->n_pages < 1) return false;
-  if ((uint64_t)p->page_tokens * p->n_pages >= (1ull << 31)) return false;
-  if (p->cache_dtype > KVC_BF16 || p->io_dtype > KVC_BF16) return false;
-  return !(p->cache_dtype == KVC_BF16 && p->io_dtype == KVC_F16);
-}
-
-// The batch's sizes (not its pointers).
-kvc_status batch_sizes(const kvc_paged_desc *p, const kvc_paged_batch *b) {
-  if (!paged_ok(p) || !b) return KVC_ERR_INVALID_ARG;
-  // one block per row or row tile: launch grids below 2^32 threads
-  if (b->n_seqs > (1u << 20) || b->n_tokens > (1u << 20)) return KVC_ERR_SHAPE;
-  if (!b->q_start && b->n_tokens != b->n_seqs) return KVC_ERR_SHAPE;
-  if (b->max_len > (1u << 30)) return KVC_ERR_SHAPE;  // a tile's end stays in 31 bits
-  if (b->n_seqs && b->max_len > (uint64_t)b->table_stride * p->page_tokens) return KVC_ERR_SHAPE;
-  return KVC_OK;
-}
-
-kvc_status batch_check(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t layer,
-                       const void *pool, const int32_t *dev_status) {
-  const kvc_status st = batch_sizes(p, b);
-  if (st != KVC_OK) return st;
-  if (layer >= p->n_layers) return KVC_ERR_SHAPE;
-  if (!pool || !aligned(pool, 16) || !dev_status || !aligned(dev_status, 4))
-    return KVC_ERR_INVALID_ARG;
-  if (b->n_seqs && (!b->lens || !aligned(b->lens, 4))) return KVC_ERR_INVALID_ARG;
-  if (b->n_seqs && b->max_len && (!b->table || !aligned(b->table, 4))) return KVC_ERR_INVALID_ARG;
-  if (b->q_start && !aligned(b->q_start, 4)) return KVC_ERR_INVALID_ARG;
-  return KVC_OK;
-}
-
-// Rows [n][heads][head_dim] `stride` elements apart.
-kvc_status rows_check(const void *p, uint64_t stride, uint32_t n, uint64_t width) {
-  if (!p || !aligned(p, 16) || stride % 8 != 0) return KVC_ERR_INVALID_ARG;
-  if (n > 1 && stride < width) return KVC_ERR_SHAPE;
-  if (stride > (1ull << 40)) return KVC_ERR_SHAPE;
-  return KVC_OK;
-}
-
-Seqs to_seqs(const kvc_paged_desc *p, const kvc_paged_batch *b) {
-  Seqs s;
-  s.table = b->table;
-  s.lens = b->lens;
-  s.q_start = b->q_start;
-  s.n_seqs = b->n_seqs;
-  s.table_stride = b->table_stride;
-  s.n_tokens = b->n_tokens;
-  s.max_len = b->max_len;
-  s.n_pages = p->n_pages;
-  s.page = FastDiv::make(p->page_tokens);
-  return s;
-}
-
-uint64_t plane_bytes(const kvc_paged_desc *p) {
-  return (uint64_t)p->n_pages * p->page_tokens * p->n_kv_heads * p->head_dim * 2;
-}
-
 kvc_status page_copy(const kvc_paged_desc *p, void *pool, const int32_t *table,
                      uint32_t table_entries, uint32_t first_token, uint32_t n_tokens, void *flat,
                      uint32_t T_total, uint32_t flat_first, bool out, int32_t *dev_status,
@@ -336,8 +313,9 @@ kvc_status page_copy(const kvc_paged_desc *p, void *pool, const int32_t *table,
 
 kvc_status attend(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t layer,
                   const void *pool, const void *q, uint64_t q_stride, float scale, uint32_t window,
-                  void *out, uint64_t out_stride, float *lse, void *ws, uint64_t ws_bytes,
-                  int32_t *dev_status, hipStream_t stream, bool prompt) {
+                  uint32_t sinks, const kvc_tree *tree, void *out, uint64_t out_stride, float *lse,
+                  void *ws, uint64_t ws_bytes, int32_t *dev_status, hipStream_t stream,
+                  bool prompt) {
   kvc_status st = batch_check(p, b, layer, pool, dev_status);
   if (st != KVC_OK) return st;
   if (prompt != (b->q_start != nullptr)) return KVC_ERR_INVALID_ARG;
@@ -350,7 +328,9 @@ kvc_status attend(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t la
   if ((st = rows_check(out, out_stride, b->n_tokens, width)) != KVC_OK) return st;
   if (q == out && q_stride != out_stride && b->n_tokens > 1) return KVC_ERR_SHAPE;
   if (!aligned(lse, 4)) return KVC_ERR_INVALID_ARG;
-  const uint64_t need = attend_ws_bytes(*p, *b);
+  if (tree && (!tree->mask || !aligned(tree->mask, 8))) return KVC_ERR_INVALID_ARG;
+  const uint32_t max_new = tree ? tree->max_tokens : 0;
+  const uint64_t need = attend_ws_bytes(*p, *b, max_new);
   if (need && (!ws || !aligned(ws, 256))) return KVC_ERR_INVALID_ARG;
   if (ws_bytes < need) return KVC_ERR_CAPACITY;
   AttendArgs a{};
@@ -370,6 +350,12 @@ kvc_status attend(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t la
   a.group_div = FastDiv::make(a.group);
   a.scale = scale_log2;
   a.window = window;
+  a.sinks = window ? std::min(sinks, 1u << 30) : 0;
+  if (tree) {
+    a.mask = tree->mask;
+    a.mask_words = (max_new + 63) / 64;
+    a.max_new = max_new;
+  }
   a.status = dev_status;
   return launch_attend(*p, *b, a, ws, stream) == hipSuccess ? KVC_OK : KVC_ERR_HIP;
 }
@@ -463,25 +449,10 @@ kvc_status kvc_append(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_
                       uint64_t v_stride, const void *q, uint64_t q_stride, void *q_out,
                       uint64_t q_out_stride, const kvc_rope *rope, int32_t *dev_status,
                       hipStream_t stream) {
-  kvc_status st = batch_check(p, b, layer, pool, dev_status);
+  const kvc_status st = append_check(p, b, layer, pool, k, k_stride, v, v_stride, q, q_stride,
+                                     q_out, q_out_stride, rope, dev_status);
   if (st != KVC_OK) return st;
-  if (rope) {
-    if (rope->reserved != 0 || rope->interleaved > 1) return KVC_ERR_INVALID_ARG;
-    if (rope->rotary_dim < 16 || rope->rotary_dim % 16 != 0 || rope->rotary_dim > p->head_dim)
-      return KVC_ERR_INVALID_ARG;
-    if (!rope->cos_sin || !aligned(rope->cos_sin, 16)) return KVC_ERR_INVALID_ARG;
-  }
-  if ((q == nullptr) != (q_out == nullptr)) return KVC_ERR_INVALID_ARG;
   if (b->n_seqs == 0 || b->n_tokens == 0) return KVC_OK;
-  const uint64_t kw = (uint64_t)p->n_kv_heads * p->head_dim;
-  const uint64_t qw = (uint64_t)p->n_heads * p->head_dim;
-  if ((st = rows_check(k, k_stride, b->n_tokens, kw)) != KVC_OK) return st;
-  if ((st = rows_check(v, v_stride, b->n_tokens, kw)) != KVC_OK) return st;
-  if (q) {
-    if ((st = rows_check(q, q_stride, b->n_tokens, qw)) != KVC_OK) return st;
-    if ((st = rows_check(q_out, q_out_stride, b->n_tokens, qw)) != KVC_OK) return st;
-    if (q == q_out && q_stride != q_out_stride) return KVC_ERR_SHAPE;
-  }
   return launch_append(*p, to_seqs(p, b), layer, pool, k, k_stride, v, v_stride, q, q_stride,
                        q_out, q_out_stride, rope, dev_status, stream) == hipSuccess
              ? KVC_OK
@@ -489,15 +460,15 @@ kvc_status kvc_append(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_
 }
 
 uint64_t kvc_attend_ws_bytes(const kvc_paged_desc *p, const kvc_paged_batch *b) {
-  return batch_sizes(p, b) == KVC_OK ? attend_ws_bytes(*p, *b) : 0;
+  return batch_sizes(p, b) == KVC_OK ? attend_ws_bytes(*p, *b, 0) : 0;
 }
 
 kvc_status kvc_attend(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t layer,
                       const void *pool, const void *q, uint64_t q_stride, float scale,
                       uint32_t window, void *out, uint64_t out_stride, float *lse, void *ws,
                       uint64_t ws_bytes, int32_t *dev_status, hipStream_t stream) {
-  return attend(p, b, layer, pool, q, q_stride, scale, window, out, out_stride, lse, ws, ws_bytes,
-                dev_status, stream, false);
+  return attend(p, b, layer, pool, q, q_stride, scale, window, 0, nullptr, out, out_stride, lse,
+                ws, ws_bytes, dev_status, stream, false);
 }
 
 kvc_status kvc_attend_prompt(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t layer,
@@ -505,8 +476,33 @@ kvc_status kvc_attend_prompt(const kvc_paged_desc *p, const kvc_paged_batch *b, 
                              uint32_t window, void *out, uint64_t out_stride, float *lse,
                              void *ws, uint64_t ws_bytes, int32_t *dev_status,
                              hipStream_t stream) {
-  return attend(p, b, layer, pool, q, q_stride, scale, window, out, out_stride, lse, ws, ws_bytes,
-                dev_status, stream, true);
+  return attend(p, b, layer, pool, q, q_stride, scale, window, 0, nullptr, out, out_stride, lse,
+                ws, ws_bytes, dev_status, stream, true);
+}
+
+kvc_status kvc_attend_sinks(const kvc_paged_desc *p, const kvc_paged_batch *b, uint32_t layer,
+                            const void *pool, const void *q, uint64_t q_stride, float scale,
+                            uint32_t window, uint32_t sinks, void *out, uint64_t out_stride,
+                            float *lse, void *ws, uint64_t ws_bytes, int32_t *dev_status,
+                            hipStream_t stream) {
+  return attend(p, b, layer, pool, q, q_stride, scale, window, sinks, nullptr, out, out_stride,
+                lse, ws, ws_bytes, dev_status, stream, b && b->q_start);
+}
+
+uint64_t kvc_attend_tree_ws_bytes(const kvc_paged_desc *p, const kvc_paged_batch *b,
+                                  const kvc_tree *tree) {
+  if (batch_sizes(p, b) != KVC_OK || !b->q_start || !tree_ok(tree)) return 0;
+  return attend_ws_bytes(*p, *b, tree->max_tokens);
+}
+
+kvc_status kvc_attend_tree(const kvc_paged_desc *p, const kvc_paged_batch *b,
+                           const kvc_tree *tree, uint32_t layer, const void *pool, const void *q,
+                           uint64_t q_stride, float scale, void *out, uint64_t out_stride,
+                           float *lse, void *ws, uint64_t ws_bytes, int32_t *dev_status,
+                           hipStream_t stream) {
+  if (!tree_ok(tree)) return KVC_ERR_INVALID_ARG;
+  return attend(p, b, layer, pool, q, q_stride, scale, 0, 0, tree, out, out_stride, lse, ws,
+                ws_bytes, dev_status, stream, true);
 }
 
 kvc_status kvc_page_out(const kvc_paged_desc *p, const void *pool, const int32_t *table,
