@@ -829,8 +829,17 @@ __device__ inline bool find_tile(const AttendArgs &a, uint32_t t, Tile &out) {
   return false;
 }
 
+// A part of a row tile's tokens: which of equal splits, or in trees which
+// steps of 2^step_shift tokens; and where its sums go (the output if it is all).
+struct Part {
+  uint32_t lo, hi, of;  // split lo of `of`; steps [lo, hi)
+  uint64_t at;
+  bool all;
+};
+
 template <class TI, class TC, int D, int NW, bool kTree>
-__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tile(AttendArgs a) {
+__device__ __forceinline__ void attend_part(const AttendArgs &a, uint8_t *lds, const Tile &t,
+                                            uint32_t hk, const Part &part) {
   constexpr int TOK = kBigTok<D>, HT = TOK / 32;
   constexpr uint32_t kThreads = NW * 64, kRows = NW * 32;
   constexpr int VB = val_bufs(NW);
@@ -839,20 +848,10 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tile(
   constexpr int CH = D / 8;         // 16-byte vectors of a row
   constexpr int TT = kThreads / TOK;  // threads to a token
   constexpr int NC = (CH + TT - 1) / TT;  // vectors each moves at most
-  extern __shared__ __align__(16) uint8_t lds[];
   uint8_t *const s_val = lds + 2 * kKeyBuf<D>;
   uint32_t *const s_odd = reinterpret_cast<uint32_t *>(s_val + VB * kValBuf<D>);  // [3][2]
   const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const uint32_t n32 = lane & 31, hi = lane >> 5;
-  const uint32_t hk = blockIdx.x % a.n_kv_heads;
-  const uint32_t rest = blockIdx.x / a.n_kv_heads;
-  const uint32_t split = rest % a.splits, tile = rest / a.splits;
-  Tile t;
-  if (blockIdx.x == 0) {
-    a.s.check(a.status);
-    if (kTree) a.s.check_new(a.max_new, a.status);
-  }
-  if (!find_tile<kRows>(a, tile, t)) return;
   const int32_t len = a.s.len(t.b);
   const uint32_t w0 = wave * 32;
   const bool busy = w0 < t.rows;  // the wave has rows
@@ -869,8 +868,11 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tile(
   const int32_t r_full = kTree ? r_first.base : r_first.hi;
   const int32_t w_full = kTree ? r_first.base : w_first.hi;
   const int32_t n_tiles = end > begin ? (end - begin + TOK - 1) / TOK : 0;
-  const int32_t t_lo = (int32_t)((int64_t)n_tiles * split / a.splits);
-  const int32_t t_hi = (int32_t)((int64_t)n_tiles * (split + 1) / a.splits);
+  constexpr uint32_t kTileShift = TOK == 64 ? 6 : 5;
+  const int32_t t_lo = kTree ? (int32_t)min((uint32_t)n_tiles, part.lo << (a.step_shift - kTileShift))
+                             : (int32_t)((int64_t)n_tiles * part.lo / part.of);
+  const int32_t t_hi = kTree ? (int32_t)min((uint32_t)n_tiles, part.hi << (a.step_shift - kTileShift))
+                             : (int32_t)((int64_t)n_tiles * (part.lo + 1) / part.of);
   const uint32_t qh = hk * a.group + row.head;
   const Scale sc_q = scale_of(a.scale);
 
@@ -1122,7 +1124,7 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tile(
   if (__ballot(bad) && lane == 0) set_status(a.status, KVC_ERR_SHAPE);
   l += other_half(l);
   if (!live) return;
-  if (a.splits == 1) {
+  if (part.all) {
     const bool some = row.hi > row.lo;
     const float inv = some ? 1.0f / l : 0.0f;
     TI *op = static_cast<TI *>(a.out) + (uint64_t)row.token * a.out_stride + (uint64_t)qh * D +
@@ -1140,8 +1142,7 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tile(
       a.lse[(uint64_t)row.token * a.n_heads + qh] =
           some ? (ref - kShiftBig<TC> + __builtin_amdgcn_logf(l)) * kLn2 : ninf();
   } else {
-    const uint64_t part = ((uint64_t)tile * a.n_kv_heads + hk) * a.splits + split;
-    float *op = a.part + (part * kRows + w0 + n32) * D + hi * 4;
+    float *op = a.part + (part.at * kRows + w0 + n32) * D + hi * 4;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -1149,10 +1150,25 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tile(
         *reinterpret_cast<f32x4 *>(op + d * 32 + i * 8) =
             f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
     if (hi == 0) {
-      a.part_ml[part * (2 * kRows) + w0 + n32] = ref;
-      a.part_ml[part * (2 * kRows) + kRows + w0 + n32] = l;
+      a.part_ml[part.at * (2 * kRows) + w0 + n32] = ref;
+      a.part_ml[part.at * (2 * kRows) + kRows + w0 + n32] = l;
     }
   }
+}
+
+template <class TI, class TC, int D, int NW>
+__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tile(AttendArgs a) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  const uint32_t hk = blockIdx.x % a.n_kv_heads;
+  const uint32_t rest = blockIdx.x / a.n_kv_heads;
+  const uint32_t split = rest % a.splits, tile = rest / a.splits;
+  Tile t;
+  if (blockIdx.x == 0) a.s.check(a.status);
+  if (!find_tile<NW * 32>(a, tile, t)) return;
+  attend_part<TI, TC, D, NW, false>(
+      a, lds, t, hk,
+      Part{split, 0, a.splits, ((uint64_t)tile * a.n_kv_heads + hk) * a.splits + split,
+           a.splits == 1});
 }
 
 // Joins the splits of k_attend_tile: a wave per (row tile, KV head, row).
@@ -1205,6 +1221,277 @@ __global__ __launch_bounds__(256) void k_attend_tile_join(AttendArgs a) {
         some ? (mm - kShiftBig<TC> + __builtin_amdgcn_logf(l)) * kLn2 : ninf();
 }
 
+// ---------------------------------------------------------- trees of new tokens
+// The same tiles, shared out as k_attend_rows does: the work of a KV head is a
+// line of steps, the sequences in order, in each its row tiles, in each its
+// tokens; as many workgroups as the chip holds take equal pieces of the heads'
+// lines, wherever the cuts fall.  A drafted tree is a few dozen rows over a long
+// cache, and caches of a batch differ by a factor of ten: cut into equal splits
+// of whole sequences, the longest one's workgroups ran on alone.
+//
+// Neighbouring workgroups take the same piece of neighbouring heads, whose rows
+// lie side by side in HBM.  A sequence's rows are shared evenly among its tiles
+// (in waves of 32), and every tile reads the keys and values again: with 256
+// rows a workgroup needs a tile of 64 tokens (32 KB at head_dim 128) every 2
+// us, a fourth of what HBM gives 256 of them, so no locality among a sequence's
+// tiles is asked for.
+
+// Piece w of `parts` pieces of a line: equal lines one after another, in as many
+// pieces each, are cut at their ends.
+struct TreePieces {
+  uint32_t parts, line;
+  __device__ uint32_t start(uint32_t w) const { return (uint32_t)((uint64_t)w * line / parts); }
+  __device__ uint32_t owner(uint32_t x) const {
+    return (uint32_t)((((uint64_t)x + 1) * parts - 1) / line);
+  }
+};
+
+// A row tile whose tokens several workgroups hold, for the join: which they are
+// and what its rows are.  One for each workgroup (whose last part alone can be
+// cut and its tile's first), or, where they are fewer, one for each tile and
+// head (`by_unit`), so that the join launches no idle workgroups.
+struct TreeInfo {
+  uint32_t cut, head, first, last, slot;  // first, last: pieces of the head
+  int32_t len;
+  Tile t;
+  uint32_t pad[5];
+};
+// The workspace's records begin with the tiles that the call has.
+struct TreeHead {
+  uint32_t tiles, pad[15];
+};
+
+template <uint32_t kRows>
+struct TreeWork {
+  uint32_t b, row0, n, tiles, steps;
+  uint32_t before, tile0;  // rows (raw) and tiles of the sequences before it
+
+  // Rows that overlap others (q_start falls somewhere) are left out, so that
+  // the tiles are no more than the host counted.
+  __device__ static uint32_t rows_of(const AttendArgs &a, uint32_t raw, uint32_t before) {
+    return before + raw <= a.s.n_tokens ? raw : 0;
+  }
+  __device__ static uint32_t tiles_of(const AttendArgs &a, uint32_t n) {
+    return (n * a.group + kRows - 1) / kRows;
+  }
+  __device__ static uint32_t steps_of(const AttendArgs &a, int32_t len) {
+    return (len > 0 ? ((uint32_t)len - 1) >> a.step_shift : 0) + 1;
+  }
+  __device__ static uint32_t saturate(uint32_t rows) { return min(rows, 1u << 21); }
+  __device__ void load(const AttendArgs &a) {
+    a.s.rows(b, row0, n);
+    const uint32_t raw = n;
+    n = rows_of(a, raw, before);
+    tiles = tiles_of(a, n);
+    steps = steps_of(a, a.s.len(b));
+    upto = saturate(before + raw);
+  }
+  // the next sequence with rows; false behind the last one
+  __device__ bool next(const AttendArgs &a) {
+    do {
+      before = upto;
+      tile0 += tiles;
+      if (++b >= a.s.n_seqs) return false;
+      load(a);
+    } while (tiles == 0);
+    return true;
+  }
+  // rows [first, first + rows) of the sequence's tile k
+  __device__ static Tile tile(const AttendArgs &a, uint32_t b, uint32_t row0, uint32_t n,
+                              uint32_t tiles, uint32_t k) {
+    const uint32_t all = n * a.group;
+    // (more tiles than waves: a last one could stay without rows)
+    const uint32_t per = tiles > kRows / 32 ? kRows : ((all + tiles - 1) / tiles + 31) & ~31u;
+    Tile t;
+    t.b = b;
+    t.row0 = row0;
+    t.n = n;
+    t.first = k * per;
+    t.rows = min(per, all - t.first);
+    return t;
+  }
+  // The sequence that holds step x of the line, with x left relative to it; or,
+  // with find false, the line's steps, and tile0 as the call's tiles.
+  __device__ bool search(const AttendArgs &a, bool find, uint32_t &x, uint32_t &total) {
+    const uint32_t lane = threadIdx.x & 63;
+    uint32_t rows0 = 0, tiles0 = 0, sum0 = 0;
+    for (uint32_t b0 = 0; b0 < a.s.n_seqs; b0 += 64) {
+      uint32_t first = 0, raw = 0;
+      int32_t length = 0;
+      if (b0 + lane < a.s.n_seqs) {
+        a.s.rows(b0 + lane, first, raw);
+        length = a.s.len(b0 + lane);
+      }
+      const uint32_t rows1 = wave_sums(raw);
+      const uint32_t mine = tiles_of(a, rows_of(a, raw, rows0 + rows1 - raw));
+      const uint32_t w = mine * steps_of(a, length);
+      const uint32_t tiles1 = wave_sums(mine), sum1 = wave_sums(w);
+      if (find) {
+        const uint64_t above = __ballot(sum0 + sum1 > x);
+        if (above) {
+          const int src = __builtin_ctzll(above);
+          b = b0 + (uint32_t)src;
+          before = saturate(rows0 + __builtin_amdgcn_readlane(rows1 - raw, src));
+          tile0 = tiles0 + __builtin_amdgcn_readlane(tiles1 - mine, src);
+          x -= sum0 + __builtin_amdgcn_readlane(sum1 - w, src);
+          load(a);
+          return true;
+        }
+      }
+      rows0 = saturate(rows0 + __builtin_amdgcn_readlane(rows1, 63));
+      tiles0 += __builtin_amdgcn_readlane(tiles1, 63);
+      sum0 += __builtin_amdgcn_readlane(sum1, 63);
+    }
+    total = sum0;
+    tile0 = tiles0;
+    return false;
+  }
+
+ private:
+  uint32_t upto;
+};
+
+template <class TI, class TC, int D, int NW>
+__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tree(AttendArgs a) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  using W = TreeWork<NW * 32>;
+  TreeHead *const head = static_cast<TreeHead *>(a.info);
+  TreeInfo *const info = reinterpret_cast<TreeInfo *>(head + 1);
+  if (head && !a.by_unit && threadIdx.x == 0) info[blockIdx.x].cut = 0;
+  if (blockIdx.x == 0) {
+    a.s.check(a.status);
+    a.s.check_new(a.max_new, a.status);
+  }
+  const uint32_t w = blockIdx.x / a.n_kv_heads, hk = blockIdx.x - w * a.n_kv_heads;
+  W u;
+  uint32_t x = 0, total = 0;
+  u.search(a, false, x, total);
+  if (head && blockIdx.x == 0 && threadIdx.x == 0) head->tiles = u.tile0;
+  // at least min_steps to a workgroup
+  const TreePieces pc{min(a.pieces, (total + a.min_steps - 1) / a.min_steps), total};
+  if (w >= pc.parts) return;
+  uint32_t at = pc.start(w);
+  const uint32_t piece = at, stop = pc.start(w + 1);
+  x = at;
+  if (!u.search(a, true, x, total)) return;
+  uint32_t k = x / u.steps, off = x - k * u.steps;
+  while (at < stop) {
+    const uint32_t left = min(u.steps - off, stop - at);
+    const bool all = left == u.steps;
+    const uint32_t slot = at == piece ? 0 : 1;
+    const Tile t = W::tile(a, u.b, u.row0, u.n, u.tiles, k);
+    attend_part<TI, TC, D, NW, true>(a, lds, t, hk,
+                                     Part{off, off + left, 0, (uint64_t)blockIdx.x * 2 + slot, all});
+    const uint32_t id = a.by_unit ? (u.tile0 + k) * a.n_kv_heads + hk : blockIdx.x;
+    if (threadIdx.x == 0 && off == 0 && head && id < a.infos) {
+      if (!all)
+        info[id] = TreeInfo{1, hk, w, pc.owner(at + u.steps - 1), slot, a.s.len(u.b), t, {}};
+      else if (a.by_unit)
+        info[id].cut = 0;
+    }
+    at += left;
+    off = 0;
+    if (at < stop && ++k == u.tiles) {
+      k = 0;
+      if (!u.next(a)) return;
+    }
+  }
+}
+
+// Joins the parts of a row tile that k_attend_tree cut.  A workgroup takes 8 / S
+// rows of a TreeInfo; a row has S groups of D / 4 lanes, which take its parts
+// in turn and are added up through LDS in a fixed order.  What it reads are the
+// parts, once: 4 D + 8 bytes for each row and part.
+template <class TI, class TC, int D, int NW, uint32_t S>
+__global__ __launch_bounds__(D * 2) void k_attend_tree_join(AttendArgs a) {
+  constexpr uint32_t kRows = NW * 32, L = D / 4, R = 8 / S;
+  constexpr int U = S == 1 ? 4 : 8;  // parts in flight to a lane
+  __shared__ float s_acc[8][D], s_l[8];
+  const TreeHead *const head = static_cast<const TreeHead *>(a.info);
+  const TreeInfo info = reinterpret_cast<const TreeInfo *>(head + 1)[blockIdx.x];
+  // records behind the call's tiles were not written
+  if (a.by_unit && blockIdx.x >= head->tiles * a.n_kv_heads) return;
+  const uint32_t r0 = blockIdx.y * R;
+  if (info.cut != 1 || r0 >= info.t.rows || info.first > info.last || info.last >= a.pieces ||
+      info.head >= a.n_kv_heads || info.t.rows > kRows)
+    return;
+  const uint32_t g = threadIdx.x / L, lane = threadIdx.x - g * L, stream = g % S;
+  const uint32_t r = r0 + g / S, rc = min(r, info.t.rows - 1);
+  const uint32_t parts = info.last - info.first + 1;
+  const auto part_of = [&](uint32_t i) {
+    return ((uint64_t)(info.first + i) * a.n_kv_heads + info.head) * 2 + (i == 0 ? info.slot : 0);
+  };
+  float m = ninf(), l = 0.0f;
+  f32x4 acc = {0, 0, 0, 0};
+  for (uint32_t i0 = stream; i0 < parts; i0 += U * S) {
+    float pm[U], pl[U];
+    f32x4 x[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {  // past the last one: the last one, unused
+      const uint64_t part = part_of(min(i0 + j * S, parts - 1));
+      pm[j] = a.part_ml[part * (2 * kRows) + rc];
+      pl[j] = a.part_ml[part * (2 * kRows) + kRows + rc];
+      x[j] = *reinterpret_cast<const f32x4 *>(a.part + (part * kRows + rc) * D + lane * 4);
+    }
+    float top = m;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (i0 + j * S >= parts) pm[j] = ninf();
+      top = __builtin_fmaxf(top, pm[j]);
+    }
+    const float ref = top == ninf() ? 0.0f : top;
+    const float alpha = __builtin_amdgcn_exp2f(m - ref);
+    m = top;
+    l *= alpha;
+    acc *= alpha;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (pm[j] == ninf()) continue;  // a part in which the row sees nothing
+      const float f = __builtin_amdgcn_exp2f(pm[j] - ref);
+      l = __builtin_fmaf(pl[j], f, l);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(x[j][e], f, acc[e]);
+    }
+  }
+  if constexpr (S > 1) {
+    static_assert(S == 8, "one row to a workgroup");
+    __shared__ float s_m[8];
+    if (lane == 0) s_m[stream] = m;
+    __syncthreads();
+    float mm = s_m[0];
+#pragma unroll
+    for (uint32_t i = 1; i < S; ++i) mm = __builtin_fmaxf(mm, s_m[i]);
+    const float f = __builtin_amdgcn_exp2f(m - (mm == ninf() ? 0.0f : mm));
+    if (lane == 0) s_l[stream] = m == ninf() ? 0.0f : l * f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s_acc[stream][lane * 4 + e] = m == ninf() ? 0.0f : acc[e] * f;
+    __syncthreads();
+    if (g != 0) return;
+    m = mm;
+    l = 0.0f;
+    acc = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (uint32_t i = 0; i < S; ++i) {
+      l += s_l[i];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] += s_acc[i][lane * 4 + e];
+    }
+  }
+  if (r >= info.t.rows) return;
+  const Row row = row_of(a, info.t, info.len, info.t.first + r);
+  const bool some = row.hi > row.lo;
+  const float inv = some ? 1.0f / l : 0.0f;
+  const uint32_t h = info.head * a.group + row.head;
+  u32x2 v;
+  v[0] = some ? pack2<TI>(acc[0] * inv, acc[1] * inv) : 0u;
+  v[1] = some ? pack2<TI>(acc[2] * inv, acc[3] * inv) : 0u;
+  *reinterpret_cast<u32x2 *>(static_cast<TI *>(a.out) + (uint64_t)row.token * a.out_stride +
+                             (uint64_t)h * D + lane * 4) = v;
+  if (lane == 0 && a.lse)
+    a.lse[(uint64_t)row.token * a.n_heads + h] =
+        some ? (m - kShiftBig<TC> + __builtin_amdgcn_logf(l)) * kLn2 : ninf();
+}
+
 // ------------------------------------------------------------------- host
 struct Plan {
   uint32_t rows;      // 16, 128 or 256 to a workgroup
@@ -1214,6 +1501,8 @@ struct Plan {
   bool by_unit;       // JoinInfo records: one for each sequence and head
   uint64_t infos;
   uint32_t shift;     // log2 of the tokens of a step
+  uint32_t pieces;     // of the line: workgroups, for trees those of a head
+  uint32_t min_steps;  // steps to a workgroup at least
   uint32_t tiles, splits;             // of k_attend_tile
   uint64_t part, part_ml, info, total;  // workspace offsets
 };
@@ -1224,9 +1513,44 @@ constexpr uint32_t kWholeSteps = 16;
 // A 16-row workgroup takes at least a step for each wave of a head.
 uint32_t min_steps(const Plan &w) { return 4 / w.wg_heads; }
 
+// Caches of at most this many tokens are not cut for a tree's rows: the tiles of
+// a cut would cost less than its join.
+constexpr uint32_t kWholeTree = 256;
+
+Plan make_tree_plan(const kvc_paged_desc &p, const kvc_paged_batch &b, uint32_t max_new) {
+  Plan w{};
+  w.wg_heads = 1;
+  const uint32_t group = p.n_heads / p.n_kv_heads;
+  const uint64_t avg = (uint64_t)b.n_tokens * group / b.n_seqs;
+  w.rows = avg <= 128 || p.head_dim == 256 ? 128 : 256;
+  w.tiles = (uint32_t)((uint64_t)b.n_tokens * group / w.rows) + std::min(b.n_seqs, b.n_tokens);
+  const uint64_t units = (uint64_t)w.tiles * p.n_kv_heads;
+  const uint32_t slots = resident(p.head_dim) * 128 / w.rows;
+  w.shift = p.head_dim == 256 ? 5 : 6;
+  const auto steps = [&]() { return std::max<uint64_t>(1, ((uint64_t)b.max_len + (1ull << w.shift) - 1) >> w.shift); };
+  const bool whole = b.max_len <= kWholeTree;
+  while (whole ? steps() > 1 : units * steps() >= (1ull << 31)) ++w.shift;
+  w.min_steps = whole ? 1 : std::max(1u, 256u >> w.shift);
+  // pieces of a head's line
+  w.pieces = (uint32_t)std::min<uint64_t>(std::max(1u, slots / p.n_kv_heads),
+                                          (w.tiles * steps() + w.min_steps - 1) / w.min_steps);
+  w.grid = w.pieces * p.n_kv_heads;
+  w.join = !whole;
+  if (w.join) {
+    w.by_unit = units < w.grid;
+    w.infos = w.by_unit ? units : w.grid;
+    w.part_ml = 2ull * w.grid * w.rows * p.head_dim * 4;
+    w.info = w.part_ml + 2ull * w.grid * w.rows * 2 * 4;
+    w.total = w.info + sizeof(TreeHead) + w.infos * sizeof(TreeInfo);
+    w.total = (w.total + 255) & ~uint64_t(255);
+  }
+  return w;
+}
+
 Plan make_plan(const kvc_paged_desc &p, const kvc_paged_batch &b, uint32_t max_new) {
   Plan w{};
   if (b.n_seqs == 0 || b.n_tokens == 0) return w;
+  if (max_new) return make_tree_plan(p, b, max_new);
   const uint32_t group = p.n_heads / p.n_kv_heads;
   const uint32_t slots = resident(p.head_dim);
   // The 16-row kernel reads a cache once for every 16 rows.  Several tokens go
@@ -1279,6 +1603,8 @@ Plan make_plan(const kvc_paged_desc &p, const kvc_paged_batch &b, uint32_t max_n
     w.join = w.splits > 1;
     parts = w.join ? units * w.splits : 0;
   }
+  w.min_steps = min_steps(w);
+  w.pieces = w.grid;
   if (w.join) {
     w.part_ml = parts * w.rows * p.head_dim * 4;
     w.info = w.part_ml + parts * w.rows * 2 * 4;
@@ -1288,10 +1614,10 @@ Plan make_plan(const kvc_paged_desc &p, const kvc_paged_batch &b, uint32_t max_n
   return w;
 }
 
-template <class TI, class TC, int D, bool kTree>
+template <class TI, class TC, int D>
 hipError_t launch_d(const AttendArgs &a, const Plan &w, hipStream_t stream) {
   const uint32_t units = w.tiles * a.n_kv_heads;
-  if constexpr (!kTree) if (w.rows == 16) {
+  if (w.rows == 16) {
     hipLaunchKernelGGL((k_attend_rows<TI, TC, D>), dim3(w.grid), dim3(256), 0, stream, a);
     if (w.join) {
       const dim3 grid((uint32_t)w.infos, std::min(kRowTile, a.group), w.wg_heads);
@@ -1304,8 +1630,25 @@ hipError_t launch_d(const AttendArgs &a, const Plan &w, hipStream_t stream) {
   }
   const auto tile = [&](auto nw) {
     constexpr int NW = decltype(nw)::value;
-    hipLaunchKernelGGL((k_attend_tile<TI, TC, D, NW, kTree>), dim3(units * w.splits),
-                       dim3(NW * 64), (kBigLds<D, NW>), stream, a);
+    if (a.mask) {
+      hipLaunchKernelGGL((k_attend_tree<TI, TC, D, NW>), dim3(w.grid), dim3(NW * 64),
+                         (kBigLds<D, NW>), stream, a);
+      if (w.join) {
+        // rows of a tile at most
+        const uint32_t rows =
+            (uint32_t)std::min<uint64_t>((uint64_t)a.max_new * a.group, NW * 32);
+        // a tile's parts are shared among a row's lanes where they are many
+        if (w.grid > 4 * units)
+          hipLaunchKernelGGL((k_attend_tree_join<TI, TC, D, NW, 8>), dim3(w.infos, rows),
+                             dim3(D * 2), 0, stream, a);
+        else
+          hipLaunchKernelGGL((k_attend_tree_join<TI, TC, D, NW, 1>), dim3(w.infos, (rows + 7) / 8),
+                             dim3(D * 2), 0, stream, a);
+      }
+      return;
+    }
+    hipLaunchKernelGGL((k_attend_tile<TI, TC, D, NW>), dim3(units * w.splits), dim3(NW * 64),
+                       (kBigLds<D, NW>), stream, a);
     if (w.join)
       hipLaunchKernelGGL((k_attend_tile_join<TI, TC, D, NW * 32>), dim3(units * (NW * 8)),
                          dim3(256), 0, stream, a);
@@ -1319,20 +1662,15 @@ hipError_t launch_d(const AttendArgs &a, const Plan &w, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <class TI, class TC, bool kTree>
-hipError_t launch_m(const kvc_paged_desc &p, const AttendArgs &a, const Plan &w,
-                    hipStream_t stream) {
-  switch (p.head_dim) {
-    case 64: return launch_d<TI, TC, 64, kTree>(a, w, stream);
-    case 96: return launch_d<TI, TC, 96, kTree>(a, w, stream);
-    case 128: return launch_d<TI, TC, 128, kTree>(a, w, stream);
-    default: return launch_d<TI, TC, 256, kTree>(a, w, stream);
-  }
-}
 template <class TI, class TC>
 hipError_t launch_t(const kvc_paged_desc &p, const AttendArgs &a, const Plan &w,
                     hipStream_t stream) {
-  return a.mask ? launch_m<TI, TC, true>(p, a, w, stream) : launch_m<TI, TC, false>(p, a, w, stream);
+  switch (p.head_dim) {
+    case 64: return launch_d<TI, TC, 64>(a, w, stream);
+    case 96: return launch_d<TI, TC, 96>(a, w, stream);
+    case 128: return launch_d<TI, TC, 128>(a, w, stream);
+    default: return launch_d<TI, TC, 256>(a, w, stream);
+  }
 }
 
 }  // namespace
@@ -1349,14 +1687,15 @@ hipError_t launch_attend(const kvc_paged_desc &p, const kvc_paged_batch &b, Atte
   a.seq_tiles = (a.group + kRowTile - 1) / kRowTile;
   a.step_shift = w.shift;
   a.by_unit = w.by_unit;
-  a.pieces = w.grid;
-  a.min_steps = min_steps(w);
+  a.pieces = w.pieces;
+  a.min_steps = w.min_steps;
+  a.infos = (uint32_t)w.infos;
   a.wg_heads = w.wg_heads;
   a.head_groups = a.n_kv_heads / w.wg_heads;
   uint8_t *base = static_cast<uint8_t *>(ws);
   a.part = reinterpret_cast<float *>(base + w.part);
   a.part_ml = reinterpret_cast<float *>(base + w.part_ml);
-  a.info = w.join && w.rows == 16 ? base + w.info : nullptr;
+  a.info = w.infos ? base + w.info : nullptr;
   if (p.io_dtype == KVC_F16) return launch_t<f16, f16>(p, a, w, stream);
   if (p.cache_dtype == KVC_BF16) return launch_t<bf16, bf16>(p, a, w, stream);
   return launch_t<bf16, f16>(p, a, w, stream);
