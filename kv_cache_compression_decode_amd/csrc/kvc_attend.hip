@@ -1398,13 +1398,266 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tree(
   }
 }
 
-// Joins the parts of a row tile that k_attend_tree cut.  A workgroup takes 8 / S
+// A tree of up to 16 R rows to a KV head: as k_attend_rows, without LDS, the
+// keys and values of 32 tokens going from HBM to registers once for all rows.
+// Each wave takes a piece of a head's line by itself; neighbouring waves the
+// same piece of neighbouring heads.
+template <class TI, class TC, int D, int R>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_few(AttendArgs a) {
+  constexpr int E = D / 16, KK = D / 32;
+  constexpr uint32_t kRows = 16 * R;
+  using W = TreeWork<kRows>;
+  const uint32_t lane = threadIdx.x & 63, n16 = lane & 15, g4 = lane >> 4;
+  const uint32_t v = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t w = v / a.n_kv_heads, hk = v - w * a.n_kv_heads;
+  TreeHead *const head = static_cast<TreeHead *>(a.info);
+  TreeInfo *const info = reinterpret_cast<TreeInfo *>(head + 1);
+  if (head && !a.by_unit && lane == 0 && v < a.infos) info[v].cut = 0;
+  if (blockIdx.x == 0) {
+    a.s.check(a.status);
+    a.s.check_new(a.max_new, a.status);
+  }
+  if (w >= a.pieces) return;
+  W u;
+  uint32_t x0 = 0, total = 0;
+  u.search(a, false, x0, total);
+  if (head && v == 0 && lane == 0) head->tiles = u.tile0;
+  const TreePieces pc{min(a.pieces, (total + a.min_steps - 1) / a.min_steps), total};
+  if (w >= pc.parts) return;
+  uint32_t at = pc.start(w);
+  const uint32_t piece = at, stop = pc.start(w + 1);
+  x0 = at;
+  if (!u.search(a, true, x0, total)) return;
+  uint32_t k = x0 / u.steps, off = x0 - k * u.steps;
+  const Scale sc_q = scale_of(a.scale);
+  const TC *const kbase = static_cast<const TC *>(a.k) + (uint64_t)hk * D;
+  const TC *const vbase = static_cast<const TC *>(a.v) + (uint64_t)hk * D;
+  bool bad = false;
+  while (at < stop) {
+    const uint32_t left = min(u.steps - off, stop - at);
+    const bool all = left == u.steps;
+    const Tile t = W::tile(a, u.b, u.row0, u.n, u.tiles, k);
+    const int32_t len = a.s.len(u.b), base = len - (int32_t)u.n, last = len - 1;
+    const int32_t tiles = len > 0 ? (int32_t)(((uint32_t)len + kTok - 1) / kTok) : 0;
+    const int32_t t_lo = min(tiles, (int32_t)(off << (a.step_shift - 5)));
+    const int32_t t_hi = min(tiles, (int32_t)((off + left) << (a.step_shift - 5)));
+    const int32_t *table = a.s.table + (uint64_t)u.b * a.s.table_stride;
+    // Each lane looks up one token of a tile, a tile ahead of its use.
+    uint32_t next_id = 0, next_in = 0;
+    auto look_up = [&](int32_t ti) {
+      int32_t j = ti * (int32_t)kTok + (int32_t)(lane & 31);
+      j = j < last ? j : last;
+      const uint32_t page = a.s.page.div((uint32_t)j);
+      next_id = (uint32_t)table[page];
+      next_in = (uint32_t)j - page * a.s.page.d;
+    };
+    if (t_lo < t_hi) look_up(t_lo);
+    float m[R], l[R];
+    f32x4 o[R][E];
+    u32x4 qf[R][KK];
+    Row row[R];
+    bool live[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      live[r] = r * 16 + n16 < t.rows;
+      row[r] = row_of(a, t, len, t.first + (live[r] ? r * 16 + n16 : 0));
+      m[r] = ninf();
+      l[r] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[r][e] = f32x4{0, 0, 0, 0};
+      const TI *q = static_cast<const TI *>(a.q) + (uint64_t)row[r].token * a.q_stride +
+                    (uint64_t)(hk * a.group + row[r].head) * D + g4 * 8;
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk)
+        qf[r][kk] = live[r] ? load_q8<TI, TC>(q + kk * 32, sc_q) : u32x4{0, 0, 0, 0};
+    }
+
+    for (int32_t ti = t_lo; ti < t_hi; ++ti) {
+      const int32_t j0 = ti * (int32_t)kTok;
+      // slots of this lane's two key rows and eight value rows
+      uint32_t slot, kslot[2], vslot[8];
+      bad = !a.s.slot_in(next_id, next_in, slot) || bad;
+      kslot[0] = __shfl(slot, n16);
+      kslot[1] = __shfl(slot, 16 + n16);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) vslot[i] = __shfl(slot, (i >> 2) * 16 + g4 * 4 + (i & 3));
+      u32x4 kf[2][KK];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const TC *kp = kbase + (uint64_t)kslot[h] * a.row + g4 * 8;
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) kf[h][kk] = load16(kp + kk * 32);
+      }
+      Words<E / 2> vf[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        vf[i] = stream_words<E / 2>(vbase + (uint64_t)vslot[i] * a.row + n16 * E);
+      if (ti + 1 < t_hi) look_up(ti + 1);
+
+      float x[R][8];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          f32x4 sc = {0, 0, 0, 0};
+#pragma unroll
+          for (int kk = 0; kk < KK; ++kk) sc = mfma16<TC>(kf[h][kk], qf[r][kk], sc);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[r][h * 4 + i] = sc[i] * sc_q.s;
+        }
+      // token of element i: (i >> 2) * 16 + g4 * 4 + (i & 3)
+      const bool edge = j0 + (int32_t)kTok > base;  // some tokens are hidden from some rows
+      uint32_t see[R], odd = 0;
+      if (edge) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          see[r] = (uint32_t)tree_sees(a, row[r], j0);
+          const uint32_t mine = see[r] >> (g4 * 4);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            x[r][i] = (mine >> ((i >> 2) * 16 + (i & 3))) & 1 ? x[r][i] : ninf();
+        }
+        // A hidden token's probability is 0, but 0 times an infinity or NaN of
+        // its value row would not be: such rows are left out of the product
+        // and added below where they are seen.
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t e0 = (i >> 2) * 16 + (i & 3);
+          bool nf = false;
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) nf = nf || nonfinite2<TC>(vf[i].w[e]);
+          const uint64_t any = __ballot(nf);
+          if (any) {
+#pragma unroll
+            for (uint32_t g = 0; g < 4; ++g)
+              if ((any >> (16 * g)) & 0xFFFF) odd |= 1u << (e0 + g * 4);
+          }
+          if ((odd >> (e0 + g4 * 4)) & 1)
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) vf[i].w[e] = 0;
+        }
+      }
+      u32x4 pf[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float mt = x[r][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) mt = __builtin_fmaxf(mt, x[r][i]);
+        mt = __builtin_fmaxf(mt, __shfl_xor(mt, 16));
+        mt = __builtin_fmaxf(mt, __shfl_xor(mt, 32));
+        const float mn = __builtin_fmaxf(m[r], mt);
+        const float ref = mn == ninf() ? 0.0f : mn;  // nothing visible yet: exp2(-inf - 0) = 0
+        const float alpha = __builtin_amdgcn_exp2f(m[r] - ref);
+        m[r] = mn;
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[r][i] = __builtin_amdgcn_exp2f(x[r][i] - ref + kShiftBig<TC>);
+          sum += x[r][i];
+        }
+        l[r] = __builtin_fmaf(l[r], alpha, sum);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pf[r][i] = pack2<TC>(x[r][2 * i], x[r][2 * i + 1]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[r][e] *= alpha;
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        u32x4 vt;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          vt[i] = __builtin_amdgcn_perm(vf[2 * i + 1].w[e / 2], vf[2 * i].w[e / 2],
+                                        (e & 1) ? 0x07060302u : 0x05040100u);
+#pragma unroll
+        for (int r = 0; r < R; ++r) o[r][e] = mfma16<TC>(vt, pf[r], o[r][e]);
+      }
+      for (; odd; odd &= odd - 1) {
+        const uint32_t jt = (uint32_t)__builtin_ctz(odd);
+        const int32_t j = j0 + (int32_t)jt;
+        uint32_t sj;
+        a.s.slot_of(table, (uint32_t)(j < last ? j : last), sj);
+        const TC *vp = vbase + (uint64_t)sj * a.row + g4 * 4 * E;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float pj = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) pj = (jt >> 4) * 4 + (jt & 3) == (uint32_t)i ? x[r][i] : pj;
+          pj = __shfl(pj, (int)(((jt >> 2) & 3) * 16 + n16));
+          if ((see[r] >> jt) & 1)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                o[r][e][c] = __builtin_fmaf(pj, (float)vp[c * E + e], o[r][e][c]);
+        }
+      }
+    }
+    const uint32_t slot = at == piece ? 0 : 1;
+    const uint64_t part = (uint64_t)v * 2 + slot;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      l[r] += __shfl_xor(l[r], 16);
+      l[r] += __shfl_xor(l[r], 32);
+      if (!live[r]) continue;
+      // a lane's 4 E values are dimensions g4 * 4 E on of its row
+      const bool some = row[r].hi > row[r].lo;
+      const float f = all ? (some ? 1.0f / l[r] : 0.0f) : 1.0f;
+      float val[4 * E];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int e = 0; e < E; ++e) val[c * E + e] = o[r][e][c] * f;
+      const uint32_t h = hk * a.group + row[r].head;
+      if (all) {
+        TI *out = static_cast<TI *>(a.out) + (uint64_t)row[r].token * a.out_stride +
+                  (uint64_t)h * D + g4 * 4 * E;
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+          u32x4 wv;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            wv[e] = some ? pack2<TI>(val[8 * i + 2 * e], val[8 * i + 2 * e + 1]) : 0u;
+          store16(out + 8 * i, wv);
+        }
+        if (g4 == 0 && a.lse)
+          a.lse[(uint64_t)row[r].token * a.n_heads + h] =
+              some ? (m[r] - kShiftBig<TC> + __builtin_amdgcn_logf(l[r])) * kLn2 : ninf();
+      } else {
+        float *op = a.part + (part * kRows + r * 16 + n16) * D + g4 * 4 * E;
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          *reinterpret_cast<f32x4 *>(op + 4 * i) =
+              f32x4{val[4 * i], val[4 * i + 1], val[4 * i + 2], val[4 * i + 3]};
+        if (g4 == 0) {
+          a.part_ml[part * (2 * kRows) + r * 16 + n16] = m[r];
+          a.part_ml[part * (2 * kRows) + kRows + r * 16 + n16] = l[r];
+        }
+      }
+    }
+    const uint32_t id = a.by_unit ? (u.tile0 + k) * a.n_kv_heads + hk : v;
+    if (lane == 0 && off == 0 && head && id < a.infos) {
+      if (!all)
+        info[id] = TreeInfo{1, hk, w, pc.owner(at + u.steps - 1), slot, len, t, {}};
+      else if (a.by_unit)
+        info[id].cut = 0;
+    }
+    at += left;
+    off = 0;
+    if (at < stop && ++k == u.tiles) {
+      k = 0;
+      if (!u.next(a)) break;
+    }
+  }
+  if (__ballot(bad) && lane == 0) set_status(a.status, KVC_ERR_SHAPE);
+}
+
+// Joins the parts of a row tile that k_attend_tree or k_attend_few cut.  A workgroup takes 8 / S
 // rows of a TreeInfo; a row has S groups of D / 4 lanes, which take its parts
 // in turn and are added up through LDS in a fixed order.  What it reads are the
 // parts, once: 4 D + 8 bytes for each row and part.
-template <class TI, class TC, int D, int NW, uint32_t S>
+template <class TI, class TC, int D, uint32_t kRows, uint32_t S>
 __global__ __launch_bounds__(D * 2) void k_attend_tree_join(AttendArgs a) {
-  constexpr uint32_t kRows = NW * 32, L = D / 4, R = 8 / S;
+  constexpr uint32_t L = D / 4, R = 8 / S;
   constexpr int U = S == 1 ? 4 : 8;  // parts in flight to a lane
   __shared__ float s_acc[8][D], s_l[8];
   const TreeHead *const head = static_cast<const TreeHead *>(a.info);
@@ -1521,26 +1774,31 @@ Plan make_tree_plan(const kvc_paged_desc &p, const kvc_paged_batch &b, uint32_t 
   Plan w{};
   w.wg_heads = 1;
   const uint32_t group = p.n_heads / p.n_kv_heads;
-  const uint64_t avg = (uint64_t)b.n_tokens * group / b.n_seqs;
-  w.rows = avg <= 128 || p.head_dim == 256 ? 128 : 256;
+  const uint64_t most = (uint64_t)max_new * group, avg = (uint64_t)b.n_tokens * group / b.n_seqs;
+  w.rows = most <= 16 ? 16 : most <= 32 ? 32 : avg <= 128 || p.head_dim == 256 ? 128 : 256;
   w.tiles = (uint32_t)((uint64_t)b.n_tokens * group / w.rows) + std::min(b.n_seqs, b.n_tokens);
   const uint64_t units = (uint64_t)w.tiles * p.n_kv_heads;
-  const uint32_t slots = resident(p.head_dim) * 128 / w.rows;
-  w.shift = p.head_dim == 256 ? 5 : 6;
-  const auto steps = [&]() { return std::max<uint64_t>(1, ((uint64_t)b.max_len + (1ull << w.shift) - 1) >> w.shift); };
+  // a tile of k_attend_few, and one of attend_part
+  const uint32_t tok = w.rows <= 32 || p.head_dim == 256 ? 5 : 6;
   const bool whole = b.max_len <= kWholeTree;
+  w.shift = tok;
+  const auto steps = [&]() {
+    return std::max<uint64_t>(1, ((uint64_t)b.max_len + (1ull << w.shift) - 1) >> w.shift);
+  };
   while (whole ? steps() > 1 : units * steps() >= (1ull << 31)) ++w.shift;
-  w.min_steps = whole ? 1 : std::max(1u, 256u >> w.shift);
-  // pieces of a head's line
-  w.pieces = (uint32_t)std::min<uint64_t>(std::max(1u, slots / p.n_kv_heads),
+  w.min_steps = whole ? 1 : std::max(1u, (w.rows <= 32 ? 128u : 256u) >> w.shift);
+  // pieces of a head's line: waves of k_attend_few, workgroups of k_attend_tree
+  const uint32_t slots = w.rows <= 32 ? resident(p.head_dim) * 4 : resident(p.head_dim) * 128 / w.rows;
+  w.pieces = (uint32_t)std::min<uint64_t>(std::min(512u, std::max(1u, slots / p.n_kv_heads)),
                                           (w.tiles * steps() + w.min_steps - 1) / w.min_steps);
-  w.grid = w.pieces * p.n_kv_heads;
-  w.join = !whole;
+  const uint32_t grid = w.pieces * p.n_kv_heads;
+  w.grid = w.rows <= 32 ? (grid + 3) / 4 : grid;
+  w.join = !whole && w.pieces > 1;
   if (w.join) {
-    w.by_unit = units < w.grid;
-    w.infos = w.by_unit ? units : w.grid;
-    w.part_ml = 2ull * w.grid * w.rows * p.head_dim * 4;
-    w.info = w.part_ml + 2ull * w.grid * w.rows * 2 * 4;
+    w.by_unit = units < grid;
+    w.infos = w.by_unit ? units : grid;
+    w.part_ml = 2ull * grid * w.rows * p.head_dim * 4;
+    w.info = w.part_ml + 2ull * grid * w.rows * 2 * 4;
     w.total = w.info + sizeof(TreeHead) + w.infos * sizeof(TreeInfo);
     w.total = (w.total + 255) & ~uint64_t(255);
   }
@@ -1614,9 +1872,35 @@ Plan make_plan(const kvc_paged_desc &p, const kvc_paged_batch &b, uint32_t max_n
   return w;
 }
 
+template <class TI, class TC, int D, uint32_t kRows>
+void launch_tree_join(const AttendArgs &a, const Plan &w, hipStream_t stream) {
+  if (!w.join) return;
+  const uint32_t rows = (uint32_t)std::min<uint64_t>((uint64_t)a.max_new * a.group, kRows);
+  const uint64_t units = (uint64_t)w.tiles * a.n_kv_heads;
+  // a tile's parts are shared among a row's lanes where they are many
+  if ((uint64_t)w.pieces * a.n_kv_heads > 4 * units)
+    hipLaunchKernelGGL((k_attend_tree_join<TI, TC, D, kRows, 8>), dim3((uint32_t)w.infos, rows),
+                       dim3(D * 2), 0, stream, a);
+  else
+    hipLaunchKernelGGL((k_attend_tree_join<TI, TC, D, kRows, 1>),
+                       dim3((uint32_t)w.infos, (rows + 7) / 8), dim3(D * 2), 0, stream, a);
+}
+
 template <class TI, class TC, int D>
 hipError_t launch_d(const AttendArgs &a, const Plan &w, hipStream_t stream) {
   const uint32_t units = w.tiles * a.n_kv_heads;
+  if (a.mask && w.rows <= 32) {
+    const auto few = [&](auto r) {
+      constexpr int R = decltype(r)::value;
+      hipLaunchKernelGGL((k_attend_few<TI, TC, D, R>), dim3(w.grid), dim3(256), 0, stream, a);
+      launch_tree_join<TI, TC, D, 16 * R>(a, w, stream);
+    };
+    if (w.rows == 16)
+      few(std::integral_constant<int, 1>{});
+    else
+      few(std::integral_constant<int, 2>{});
+    return hipGetLastError();
+  }
   if (w.rows == 16) {
     hipLaunchKernelGGL((k_attend_rows<TI, TC, D>), dim3(w.grid), dim3(256), 0, stream, a);
     if (w.join) {
@@ -1633,18 +1917,7 @@ hipError_t launch_d(const AttendArgs &a, const Plan &w, hipStream_t stream) {
     if (a.mask) {
       hipLaunchKernelGGL((k_attend_tree<TI, TC, D, NW>), dim3(w.grid), dim3(NW * 64),
                          (kBigLds<D, NW>), stream, a);
-      if (w.join) {
-        // rows of a tile at most
-        const uint32_t rows =
-            (uint32_t)std::min<uint64_t>((uint64_t)a.max_new * a.group, NW * 32);
-        // a tile's parts are shared among a row's lanes where they are many
-        if (w.grid > 4 * units)
-          hipLaunchKernelGGL((k_attend_tree_join<TI, TC, D, NW, 8>), dim3(w.infos, rows),
-                             dim3(D * 2), 0, stream, a);
-        else
-          hipLaunchKernelGGL((k_attend_tree_join<TI, TC, D, NW, 1>), dim3(w.infos, (rows + 7) / 8),
-                             dim3(D * 2), 0, stream, a);
-      }
+      launch_tree_join<TI, TC, D, NW * 32>(a, w, stream);
       return;
     }
     hipLaunchKernelGGL((k_attend_tile<TI, TC, D, NW>), dim3(units * w.splits), dim3(NW * 64),

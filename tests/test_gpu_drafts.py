@@ -138,6 +138,9 @@ TREES = [
     (3, 3, 96, 5, BF16, BF16, [800, 32], [32, 3]),
     (3, 3, 256, 16, F16, F16, [640, 33], [33, 12]),
     (12, 6, 256, 16, BF16, F16, [1030, 14], [8, 7]),
+    (4, 2, 256, 16, F16, F16, [500, 40, 1200], [16, 9, 13]),
+    (10, 5, 128, 16, BF16, BF16, [2500, 40, 1200, 16], [16, 9, 13, 16]),
+    (24, 1, 128, 16, F16, F16, [5000], [1]),
     # sequences that begin with the tree's tokens, padding among them
     (4, 2, 64, 16, F16, F16, [20, 9, 3], [20, 12, 5]),
     # many sequences
