@@ -1775,7 +1775,11 @@ Plan make_tree_plan(const kvc_paged_desc &p, const kvc_paged_batch &b, uint32_t 
   w.wg_heads = 1;
   const uint32_t group = p.n_heads / p.n_kv_heads;
   const uint64_t most = (uint64_t)max_new * group, avg = (uint64_t)b.n_tokens * group / b.n_seqs;
-  w.rows = most <= 16 ? 16 : most <= 32 ? 32 : avg <= 128 || p.head_dim == 256 ? 128 : 256;
+  // (32 rows of 256 dimensions would not fit the registers)
+  w.rows = most <= 16                         ? 16
+           : most <= 32 && p.head_dim != 256  ? 32
+           : avg <= 128 || p.head_dim == 256  ? 128
+                                              : 256;
   w.tiles = (uint32_t)((uint64_t)b.n_tokens * group / w.rows) + std::min(b.n_seqs, b.n_tokens);
   const uint64_t units = (uint64_t)w.tiles * p.n_kv_heads;
   // a tile of k_attend_few, and one of attend_part
@@ -1895,10 +1899,12 @@ hipError_t launch_d(const AttendArgs &a, const Plan &w, hipStream_t stream) {
       hipLaunchKernelGGL((k_attend_few<TI, TC, D, R>), dim3(w.grid), dim3(256), 0, stream, a);
       launch_tree_join<TI, TC, D, 16 * R>(a, w, stream);
     };
-    if (w.rows == 16)
-      few(std::integral_constant<int, 1>{});
-    else
-      few(std::integral_constant<int, 2>{});
+    if constexpr (D != 256)
+      if (w.rows == 32) {
+        few(std::integral_constant<int, 2>{});
+        return hipGetLastError();
+      }
+    few(std::integral_constant<int, 1>{});
     return hipGetLastError();
   }
   if (w.rows == 16) {

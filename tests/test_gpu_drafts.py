@@ -155,6 +155,18 @@ def test_attend_tree(heads, kv_heads, head_dim, page, io, cache, lens, new):
     st.check(*st.attend())
 
 
+@pytest.mark.parametrize("head_dim", [64, 96, 128, 256])
+@pytest.mark.parametrize("most,group", [(4, 4), (8, 4), (12, 4), (50, 4)])
+def test_attend_tree_many_sequences_to_a_piece(head_dim, most, group):
+    """Sequences of every length from none to a few tiles, several in each
+    workgroup's or wave's share, with long ones between them that are cut."""
+    lens = [0, 5, 40, 90, 33, 64, 65, 1, 700, 31, 32, 100, 12, 1500, 95, 47, 16, 63, 130, 2]
+    new = [min(m, 1 + (7 * i) % most) if m else i % 3 for i, m in enumerate(lens)]
+    new[13] = most
+    st = Drafts(lens, new, 2 * group, 2, head_dim, 16, F16, F16)
+    st.check(*st.attend())
+
+
 @pytest.mark.parametrize("kind", ["chain", "star"])
 @pytest.mark.parametrize("n,group", [(7, 1), (70, 1), (40, 8)])
 def test_attend_tree_shapes(kind, n, group):
