@@ -16,6 +16,7 @@ uint64_t row_bytes(const kvc_paged_desc *p) { return (uint64_t)p->n_kv_heads * p
 // and never stores over a row that it has still to load.  Each byte moved is
 // read and written once; lanes lie along the row.
 constexpr uint32_t kKeepRows = 8;
+constexpr uint32_t kKeepBlocks = 2048;
 
 struct KeepArgs {
   Seqs s;
@@ -30,7 +31,8 @@ struct KeepArgs {
 };
 
 __global__ __launch_bounds__(256) void k_keep(KeepArgs a) {
-  __shared__ uint32_t s_from[kTreeTokens], s_to[kTreeTokens];
+  extern __shared__ uint32_t s_from[];  // [path_stride]
+  uint32_t *const s_to = s_from + a.path_stride;
   const uint32_t b = blockIdx.x;
   uint32_t row0, n;
   a.s.rows(b, row0, n);
@@ -191,6 +193,7 @@ __global__ __launch_bounds__(1024) void k_resize(LedgerArgs a, const int32_t *ne
   __shared__ uint32_t s_off[kRows];
   __shared__ uint64_t s_wave[16];
   __shared__ uint32_t s_free[kScan * 16];
+  __shared__ int32_t s_found[kRows];  // the first pages found; more go to `found`
   const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   bool bad = false;
   for (uint32_t r = threadIdx.x; r < a.n_rows; r += 1024) {
@@ -211,8 +214,7 @@ __global__ __launch_bounds__(1024) void k_resize(LedgerArgs a, const int32_t *ne
       bad = !a.release(ids[e]) || bad;
     if (lane == 0) a.lens[r] = now;
   }
-  __threadfence();
-  __syncthreads();
+  __syncthreads();  // each release has its answer by now
   // Shared pages that a row would grow into.  Row by row, each takes a copy
   // while more than one holds the page; so the last of them may keep it.
   int32_t shared[2] = {0, 0};
@@ -240,15 +242,19 @@ __global__ __launch_bounds__(1024) void k_resize(LedgerArgs a, const int32_t *ne
     if (r < a.n_rows && s_new[r] > s_old[r]) {
       if (s_page[r] >= 0) {
         int32_t left = shared[k];
+#pragma unroll 8
         for (uint32_t j = 0; j < r; ++j) left -= s_page[j] == s_page[r];
         copy = left > 1;
       }
       need[k] = a.pages_of(s_new[r]) - a.pages_of(s_old[r]) + (copy ? 1u : 0u);
       if (copy) need[k] |= 1ull << 48;
     }
-    uint64_t t;
-    upto[k] = block_sums(need[k], s_wave, t) + total;
-    total += t;
+    upto[k] = total;
+    if (k * 1024u < a.n_rows) {
+      uint64_t t;
+      upto[k] += block_sums(need[k], s_wave, t);
+      total += t;
+    }
   }
   const uint64_t want = total & ((1ull << 48) - 1);
   uint64_t have = 0;
@@ -277,7 +283,13 @@ __global__ __launch_bounds__(1024) void k_resize(LedgerArgs a, const int32_t *ne
     for (uint32_t k = 0; k < kScan; ++k) {
       const uint64_t pos = have + s_free[k * 16 + wave] +
                            __popcll(free[k] & ((1ull << lane) - 1));
-      if ((free[k] >> lane) & 1 && pos < want) found[pos] = (int32_t)(at + k * 1024 + threadIdx.x);
+      if ((free[k] >> lane) & 1 && pos < want) {
+        const int32_t id = (int32_t)(at + k * 1024 + threadIdx.x);
+        if (pos < kRows)
+          s_found[pos] = id;
+        else
+          found[pos] = id;
+      }
     }
     have += t;
   }
@@ -303,9 +315,8 @@ __global__ __launch_bounds__(1024) void k_resize(LedgerArgs a, const int32_t *ne
     }
     s_off[r] = off;
   }
-  __threadfence();
   __syncthreads();
-  // (the copies' new pages come through `found`, written by other threads)
+  const auto page_at = [&](uint32_t i) { return i < kRows ? s_found[i] : found[i]; };
   for (uint32_t r = wave; r < a.n_rows; r += 16) {
     const int32_t old = s_old[r], now = s_new[r];
     if (now <= old) continue;
@@ -314,7 +325,7 @@ __global__ __launch_bounds__(1024) void k_resize(LedgerArgs a, const int32_t *ne
     if (s_page[r] >= 0) {
       if (lane == 0) {
         Copy &c = plan->copy[s_page[r]];
-        const int32_t id = found[off];
+        const int32_t id = page_at(off);
         c.to = id;
         ids[a.page.div((uint32_t)old)] = id;
         a.refs[id] = 1;
@@ -324,7 +335,7 @@ __global__ __launch_bounds__(1024) void k_resize(LedgerArgs a, const int32_t *ne
     }
     const uint32_t e0 = a.pages_of(old), e1 = a.pages_of(now);
     for (uint32_t e = e0 + lane; e < e1; e += 64) {
-      const int32_t id = found[off + (e - e0)];
+      const int32_t id = page_at(off + (e - e0));
       ids[e] = id;
       a.refs[id] = 1;
     }
@@ -423,8 +434,8 @@ kvc_status kvc_keep(const kvc_paged_desc *p, const kvc_paged_batch *b, void *poo
   a.status = dev_status;
   // workgroups over a sequence's items: all of them, unless sequences are many
   const uint32_t y = (uint32_t)std::min<uint64_t>((items + 255) / 256,
-                                                  std::max(1u, (1u << 14) / b->n_seqs));
-  hipLaunchKernelGGL(k_keep, dim3(b->n_seqs, y), dim3(256), 0, stream, a);
+                                                  std::max(1u, kKeepBlocks / b->n_seqs));
+  hipLaunchKernelGGL(k_keep, dim3(b->n_seqs, y), dim3(256), path_stride * 8, stream, a);
   return hipGetLastError() == hipSuccess ? KVC_OK : KVC_ERR_HIP;
 }
 
