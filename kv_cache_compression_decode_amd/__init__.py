@@ -1088,12 +1088,13 @@ def append_async(desc: PagedDesc, batch: PagedBatch, layer: int, pool: torch.Ten
     if rope is not None and rope.cos_sin.device != dev:
         raise ValueError("the rotation table must be on the batch's device")
     _workspace_check(wsp, dev)
-    args = (desc, batch._args(desc, n), layer, _pool_ptr(desc, pool, dev), k.data_ptr(), ks,
-            v.data_ptr(), vs, None if q is None else q.data_ptr(), qs,
-            None if q is None else q_out.data_ptr(), os_, None if rope is None else rope._args())
     if norm is None and tree is None:
-        _check(lib().kvc_append(*args, wsp.status.data_ptr(), _paged_stream(stream, dev)),
-               "kvc_append")
+        _check(lib().kvc_append(desc, batch._args(desc, n), layer, _pool_ptr(desc, pool, dev),
+                                k.data_ptr(), ks, v.data_ptr(), vs,
+                                None if q is None else q.data_ptr(), qs,
+                                None if q is None else q_out.data_ptr(), os_,
+                                None if rope is None else rope._args(), wsp.status.data_ptr(),
+                                _paged_stream(stream, dev)), "kvc_append")
         return
     if norm is not None and (norm.k_weight.shape[0] != dim or norm.k_weight.device != dev):
         raise ValueError("the norms' weights must have head_dim entries, on the batch's device")
@@ -1101,7 +1102,12 @@ def append_async(desc: PagedDesc, batch: PagedBatch, layer: int, pool: torch.Ten
         tree._check(n, dev)
         if batch.q_start is None:
             raise ValueError("a tree needs a batch with q_start")
-    _check(lib().kvc_append_norm(*args, None if norm is None else norm._args(),
+    _check(lib().kvc_append_norm(desc, batch._args(desc, n), layer, _pool_ptr(desc, pool, dev),
+                                 k.data_ptr(), ks, v.data_ptr(), vs,
+                                 None if q is None else q.data_ptr(), qs,
+                                 None if q is None else q_out.data_ptr(), os_,
+                                 None if rope is None else rope._args(),
+                                 None if norm is None else norm._args(),
                                  None if tree is None else tree.depth.data_ptr(),
                                  wsp.status.data_ptr(), _paged_stream(stream, dev)),
            "kvc_append_norm")

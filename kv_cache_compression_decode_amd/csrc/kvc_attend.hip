@@ -769,6 +769,11 @@ __device__ inline Row row_of(const AttendArgs &a, const Tile &t, int32_t len, ui
   return w;
 }
 
+// The lowest n bits; none or all where n is outside [0, 64].
+__device__ inline uint64_t ones(int32_t n) {
+  return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+
 // Which of the 64 tokens from j0 on a row of a tree sees; needs j0 + 64 >
 // base (all before are seen).  A row sees itself whatever its mask says, and
 // nothing behind itself.
@@ -784,9 +789,9 @@ __device__ inline uint64_t tree_sees(const AttendArgs &a, const Row &row, int32_
     see = word(k) >> sh;
     if (sh) see |= word(k + 1) << (64 - sh);
   }
-  const int32_t self = row.i - t0, n = row.hi - j0;
-  if (self >= 0 && self < 64) see |= 1ull << self;
-  return n <= 0 ? 0 : n < 64 ? see & ((1ull << n) - 1) : see;
+  const int32_t self = row.i - t0;
+  see |= (uint64_t)(self >= 0 && self < 64) << (self & 63);
+  return see & ones(row.hi - j0);
 }
 
 // Row tile `t` of the call: the sequences in order, of each its last tile (the
@@ -837,9 +842,14 @@ struct Part {
   bool all;
 };
 
-template <class TI, class TC, int D, int NW, bool kTree>
+// What a row sees: up to its position (and of that a window), also sinks, or a
+// tree's mask.
+enum Mask { kCausal, kSinks, kTreeMask };
+
+template <class TI, class TC, int D, int NW, Mask kMask>
 __device__ __forceinline__ void attend_part(const AttendArgs &a, uint8_t *lds, const Tile &t,
                                             uint32_t hk, const Part &part) {
+  constexpr bool kTree = kMask == kTreeMask;
   constexpr int TOK = kBigTok<D>, HT = TOK / 32;
   constexpr uint32_t kThreads = NW * 64, kRows = NW * 32;
   constexpr int VB = val_bufs(NW);
@@ -861,8 +871,10 @@ __device__ __forceinline__ void attend_part(const AttendArgs &a, uint8_t *lds, c
   const Row w_first = row_of(a, t, len, t.first + (busy ? w0 : 0));
   const Row w_last = row_of(a, t, len, t.first + (busy ? min(w0 + 31, t.rows - 1) : 0));
   // r_first's window is the first to begin; the sinks before it (token_of)
-  const int32_t lo = r_first.lo, begin = lo - (int32_t)min((uint32_t)lo, a.sinks);
-  const int32_t sink_end = a.sinks ? max(lo, (int32_t)a.sinks) : begin;  // tokens below: sinks
+  const int32_t lo = r_first.lo;
+  const int32_t begin = kMask == kSinks ? lo - (int32_t)min((uint32_t)lo, a.sinks) : lo;
+  // tokens below are sinks
+  const int32_t sink_end = kMask == kSinks ? max(lo, (int32_t)a.sinks) : begin;
   const int32_t end = r_last.hi, last = end - 1;
   // tokens below are seen by every row of the workgroup, of the wave
   const int32_t r_full = kTree ? r_first.base : r_first.hi;
@@ -906,7 +918,8 @@ __device__ __forceinline__ void attend_part(const AttendArgs &a, uint8_t *lds, c
   uint32_t next_id = 0, next_in = 0;  // page id; token within the page
   auto look_up = [&](int32_t ti) {
     int32_t j = begin + ti * TOK + (int32_t)my_t;
-    j = token_of(j < last ? j : last, lo, begin);
+    j = j < last ? j : last;
+    if (kMask == kSinks) j = token_of(j, lo, begin);
     const uint32_t page = a.s.page.div((uint32_t)j);
     next_id = (uint32_t)table[page];
     next_in = (uint32_t)j - page * a.s.page.d;
@@ -1015,7 +1028,7 @@ __device__ __forceinline__ void attend_part(const AttendArgs &a, uint8_t *lds, c
       pending = false;
     }
     // a wave has nothing to do where none of its rows sees a token
-    if (busy && j0 < w_last.hi && (j0 + TOK > w_first.lo || j0 < sink_end)) {
+    if (busy && j0 < w_last.hi && (j0 + TOK > w_first.lo || (kMask == kSinks && j0 < sink_end))) {
       // the matrix unit's feeder goes first where another wave has vector work
       __builtin_amdgcn_s_setprio(1);
       f32x16 s[HT];
@@ -1041,10 +1054,11 @@ __device__ __forceinline__ void attend_part(const AttendArgs &a, uint8_t *lds, c
         }
         __builtin_amdgcn_sched_group_barrier(0x8, depth, 0);
       }
-      uint64_t see = 0;
+      uint64_t see = ~0ull;
       if (j0 < w_last.lo || j0 + TOK > w_full) {
-        if constexpr (kTree) {
-          see = tree_sees(a, row, j0);
+        if constexpr (kMask != kCausal) {
+          see = kTree ? tree_sees(a, row, j0)
+                      : ones(row.hi - j0) & (~ones(row.lo - j0) | ones(sink_end - j0));
           const uint64_t mine = see >> (hi * 4);
 #pragma unroll
           for (int h = 0; h < HT; ++h)
@@ -1057,7 +1071,7 @@ __device__ __forceinline__ void attend_part(const AttendArgs &a, uint8_t *lds, c
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const int32_t j = j0 + h * 32 + (i >> 2) * 8 + (int32_t)hi * 4 + (i & 3);
-              s[h][i] = (j >= row.lo || j < sink_end) && j < row.hi ? s[h][i] : ninf();
+              s[h][i] = j >= row.lo && j < row.hi ? s[h][i] : ninf();
             }
         }
       }
@@ -1094,8 +1108,9 @@ __device__ __forceinline__ void attend_part(const AttendArgs &a, uint8_t *lds, c
         pj = __shfl(pj, (int)(n32 + 32 * ((e >> 2) & 1)));
         const int32_t j = j0 + (int32_t)jt;
         uint32_t sj;
-        a.s.slot_of(table, (uint32_t)token_of(j < last ? j : last, lo, begin), sj);
-        if (kTree ? (see >> jt) & 1 : (j >= row.lo || j < sink_end) && j < row.hi) {
+        const int32_t jc = j < last ? j : last;
+        a.s.slot_of(table, (uint32_t)(kMask == kSinks ? token_of(jc, lo, begin) : jc), sj);
+        if (kMask != kCausal ? (see >> jt) & 1 : j >= row.lo && j < row.hi) {
           const TC *vp = vbase + (uint64_t)sj * a.row + hi * 4;
 #pragma unroll
           for (int d = 0; d < DT; ++d)
@@ -1156,7 +1171,7 @@ __device__ __forceinline__ void attend_part(const AttendArgs &a, uint8_t *lds, c
   }
 }
 
-template <class TI, class TC, int D, int NW>
+template <class TI, class TC, int D, int NW, Mask kMask>
 __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tile(AttendArgs a) {
   extern __shared__ __align__(16) uint8_t lds[];
   const uint32_t hk = blockIdx.x % a.n_kv_heads;
@@ -1165,7 +1180,7 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tile(
   Tile t;
   if (blockIdx.x == 0) a.s.check(a.status);
   if (!find_tile<NW * 32>(a, tile, t)) return;
-  attend_part<TI, TC, D, NW, false>(
+  attend_part<TI, TC, D, NW, kMask>(
       a, lds, t, hk,
       Part{split, 0, a.splits, ((uint64_t)tile * a.n_kv_heads + hk) * a.splits + split,
            a.splits == 1});
@@ -1380,8 +1395,8 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tree(
     const bool all = left == u.steps;
     const uint32_t slot = at == piece ? 0 : 1;
     const Tile t = W::tile(a, u.b, u.row0, u.n, u.tiles, k);
-    attend_part<TI, TC, D, NW, true>(a, lds, t, hk,
-                                     Part{off, off + left, 0, (uint64_t)blockIdx.x * 2 + slot, all});
+    attend_part<TI, TC, D, NW, kTreeMask>(
+        a, lds, t, hk, Part{off, off + left, 0, (uint64_t)blockIdx.x * 2 + slot, all});
     const uint32_t id = a.by_unit ? (u.tile0 + k) * a.n_kv_heads + hk : blockIdx.x;
     if (threadIdx.x == 0 && off == 0 && head && id < a.infos) {
       if (!all)
@@ -1926,8 +1941,9 @@ hipError_t launch_d(const AttendArgs &a, const Plan &w, hipStream_t stream) {
       launch_tree_join<TI, TC, D, NW * 32>(a, w, stream);
       return;
     }
-    hipLaunchKernelGGL((k_attend_tile<TI, TC, D, NW>), dim3(units * w.splits), dim3(NW * 64),
-                       (kBigLds<D, NW>), stream, a);
+    const auto kernel = a.sinks ? k_attend_tile<TI, TC, D, NW, kSinks>
+                                : k_attend_tile<TI, TC, D, NW, kCausal>;
+    hipLaunchKernelGGL(kernel, dim3(units * w.splits), dim3(NW * 64), (kBigLds<D, NW>), stream, a);
     if (w.join)
       hipLaunchKernelGGL((k_attend_tile_join<TI, TC, D, NW * 32>), dim3(units * (NW * 8)),
                          dim3(256), 0, stream, a);
