@@ -142,7 +142,9 @@ __device__ inline bool nonfinite2(uint32_t w) {
   return (w & e) == e || (w & (e << 16)) == (e << 16);
 }
 
-// A row's visible tokens are counted in one run, sinks included: the s sinks
+// A row's visible tokens are counted in one run, sinks included (a batch of 45
+// with windows of 4,096 and 16 sinks, 693 MB, runs at 6.1 TB/s in k_attend_rows,
+// as without sinks): the s sinks
 // that its window, from token lo on, does not reach stand for the tokens
 // [lo - s, lo), so that only a token's lookup knows of the gap between them.
 __device__ inline int32_t token_of(int32_t j, int32_t lo, int32_t first) {
@@ -1247,9 +1249,15 @@ __global__ __launch_bounds__(256) void k_attend_tile_join(AttendArgs a) {
 // Neighbouring workgroups take the same piece of neighbouring heads, whose rows
 // lie side by side in HBM.  A sequence's rows are shared evenly among its tiles
 // (in waves of 32), and every tile reads the keys and values again: with 256
-// rows a workgroup needs a tile of 64 tokens (32 KB at head_dim 128) every 2
-// us, a fourth of what HBM gives 256 of them, so no locality among a sequence's
-// tiles is asked for.
+// rows a workgroup needs a tile of 64 tokens (32 KB at head_dim 128) every 2.7
+// us, half of what HBM gives 256 of them, so no locality among a sequence's tiles
+// is asked for.
+//
+// 15 trees of 17 to 60 tokens over 1,500 to 16,000, 8 heads to each of 8 KV heads
+// (156 GFLOP): 264 us (331 in equal splits of whole sequences; 300 with 128-row
+// tiles).  The matrix units are busy 27% of it and the vector units as much;
+// 27% of the tiles' rows are empty.  Steps weighted by their tile's waves moved
+// the cuts but gained nothing.
 
 // Piece w of `parts` pieces of a line: equal lines one after another, in as many
 // pieces each, are cut at their ends.
@@ -1416,7 +1424,9 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 8 / NW) void k_attend_tree(
 // A tree of up to 16 R rows to a KV head: as k_attend_rows, without LDS, the
 // keys and values of 32 tokens going from HBM to registers once for all rows.
 // Each wave takes a piece of a head's line by itself; neighbouring waves the
-// same piece of neighbouring heads.
+// same piece of neighbouring heads.  HBM bounds it: 12 trees of 1 to 8 tokens over
+// 900 to 9,000, 32 heads x 128 (562 MB), 92 us, 6.1 TB/s (k_attend_tree with
+// 128-row tiles: 114).
 template <class TI, class TC, int D, int R>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_few(AttendArgs a) {
   constexpr int E = D / 16, KK = D / 32;

@@ -459,3 +459,30 @@ def test_drafts_captured_and_replayed():
             assert torch.equal(a.view(torch.int16), b.view(torch.int16))
         assert bool((mine[2] != 0).any())
     kvc.read_status(mine[4].status, "graph")
+
+
+def test_drafts_on_another_stream():
+    """Every call on a stream of its own, against the current stream's."""
+    st = Drafts([700, 90], [20, 12], 8, 2, 64, 16, F16, F16)
+    w = torch.ones(64, device=DEV)
+    norm, rope = kvc.HeadNorm(w, w), kvc.Rope(kvc.rope_table(800, 64))
+    path = torch.tensor([[0, 3, 7], [0, 1, 11]], dtype=torch.int32, device=DEV)
+    kept = torch.tensor([3, 2], dtype=torch.int32, device=DEV)
+    results = []
+    for stream in (None, torch.cuda.Stream()):
+        pool, q = st.pool.clone(), torch.zeros(st.q.shape, dtype=F16, device=DEV)
+        out = torch.zeros_like(q)
+        new_lens = torch.zeros(2, dtype=torch.int32, device=DEV)
+        tree = kvc.Tree(st.tree.parent, 20)
+        wsp = kvc.PagedWorkspace(st.desc, st.batch, st.n_tok, tree=tree)
+        kvc.tree_async(st.desc, st.batch, tree, wsp, stream=stream)
+        kvc.append_async(st.desc, st.batch, 1, pool, st.k, st.v, wsp, rope=rope, q=st.q, q_out=q,
+                         norm=norm, tree=tree, stream=stream)
+        kvc.attend_tree_async(st.desc, st.batch, tree, 1, pool, q, out, wsp, stream=stream)
+        kvc.keep_async(st.desc, st.batch, pool, path, kept, new_lens, st.n_tok, wsp.status,
+                       stream=stream)
+        kvc.read_status(wsp.status, "drafts", stream)
+        results.append((pool.view(torch.int16), q, out, new_lens))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    assert bool((results[0][2] != 0).any())

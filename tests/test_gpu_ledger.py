@@ -248,3 +248,52 @@ def test_captured_and_replayed():
         graph.replay()
         torch.cuda.synchronize()
         st.check()
+
+
+def test_pages_past_four_giga_elements():
+    """Copy on write, a tree's attention and its kept path in pages whose
+    elements pass 2^32, against the same in a small pool."""
+    heads, kv_heads, dim, page, m, n = 16, 8, 128, 16, 75, 12
+    g = torch.Generator(device=DEV)
+    g.manual_seed(8)
+    flat = torch.randn((1, 2, m + n, kv_heads * dim), generator=g, device=DEV).half()
+    q = torch.randn((2 * n, heads, dim), generator=g, device=DEV).half()
+    parent = _i32([max(i - 1 - i % 3, -1) for i in range(n)] * 2)
+    results = []
+    for n_pages in (20, 280000):
+        desc = kvc.make_paged_desc(1, heads, kv_heads, dim, page, n_pages)
+        pool = torch.empty(desc.pool_shape, dtype=torch.float16, device=DEV)
+        refs = torch.ones(n_pages, dtype=torch.int32, device=DEV)
+        refs[-20:] = 0
+        table, lens = torch.full((2, 8), -1, dtype=torch.int32, device=DEV), _i32([0, 0])
+        ledger = kvc.PageLedger(desc, table, lens, refs)
+        kvc.resize_async(ledger, pool, _i32([m, 0]))
+        kvc.page_in_async(desc, flat, 0, pool, table[0], 0, m, ledger.status)
+        kvc.fork_async(ledger, _i32([0]), _i32([1]))
+        kvc.resize_async(ledger, pool, _i32([m + n] * 2))
+        batch = kvc.PagedBatch(table, lens, q_start=_i32([0, n, 2 * n]))
+        tree = kvc.Tree(parent, n)
+        wsp = kvc.PagedWorkspace(desc, batch, 2 * n, tree=tree)
+        kvc.tree_async(desc, batch, tree, wsp)
+        kv = flat[0, :, m:].view(2, n, kv_heads, dim).repeat(1, 2, 1, 1)
+        kvc.append_async(desc, batch, 0, pool, kv[0], kv[1], wsp, tree=tree)
+        out = torch.empty_like(q)
+        kvc.attend_tree_async(desc, batch, tree, 0, pool, q, out, wsp)
+        new_lens = _i32([0, 0])
+        kvc.keep_async(desc, batch, pool, _i32([[0, 5, 11], [2, 3, 4]]), _i32([3, 3]), new_lens,
+                       2 * n, wsp.status)
+        kvc.read_status(wsp.status, "far")
+        kvc.read_status(ledger.status, "far")
+        rows = []
+        for b in range(2):
+            got = torch.empty((1, 2, m + 3, kv_heads * dim), dtype=torch.float16, device=DEV)
+            kvc.page_out_async(desc, pool, table[b], 0, m + 3, got, 0, ledger.status)
+            rows.append(got)
+            want = torch.cat([flat[:, :, :m], flat[:, :, [m + t for t in
+                                                          ([0, 5, 11], [2, 3, 4])[b]]]], 2)
+            assert torch.equal(got, want)
+        assert int(table[0, 0]) == n_pages - 20 and len(set(table[:, 4].tolist())) == 2
+        results.append((out, *rows))
+        del pool
+    for a, b in zip(*results):
+        assert torch.equal(a, b)

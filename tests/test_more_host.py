@@ -156,8 +156,12 @@ def test_keep_refusals(L):
     assert _keep(L, stride=4097) == SHAPE
     for p in ("pool", "path", "kept", "new_lens", "status"):
         assert _keep(L, **{p: None}) == INVALID and _keep(L, **{p: A + 2}) == INVALID
-    for at in (A, A + 4, A + 8, A - 8):  # lens has three entries at A
-        assert _keep(L, new_lens=at) == SHAPE
+    for at in (A, A + 4, A + 8, A - 8):  # lens, kept and path: three entries at A
+        assert _keep(L, new_lens=at, kept=4 * A, path=5 * A) == SHAPE
+        assert _keep(L, b=_trees(lens=3 * A), new_lens=at, path=5 * A) == SHAPE
+        assert _keep(L, b=_trees(lens=3 * A), new_lens=at, kept=4 * A) == SHAPE
+    # the last of path's 3 * 4 entries
+    assert _keep(L, b=_trees(lens=3 * A), new_lens=A + 44, kept=4 * A) == SHAPE
     wide = _desc(n_layers=32767, n_heads=4096, n_kv_heads=4096, head_dim=256, page_tokens=1)
     assert _keep(L, d=wide) == SHAPE
 
@@ -189,6 +193,20 @@ def test_empty_calls_do_nothing(L):
     assert _fork(L, n=0, src=None, dst=None) == 0
     nothing = _ledger(None, None, None, 0, 0)
     assert _fork(L, g=nothing, n=0) == 0 and _resize(L, g=nothing, lens=None, ws=None) == 0
+
+
+@pytest.mark.parametrize("head_dim", [64, 96, 128, 256])
+@pytest.mark.parametrize("heads,kv_heads", [(8, 8), (64, 8), (128, 1), (6, 2), (4096, 4096)])
+def test_tree_workspace_bound(L, head_dim, heads, kv_heads):
+    """The documented bound holds for every batch."""
+    d = _desc(n_heads=heads, n_kv_heads=kv_heads, head_dim=head_dim)
+    for seqs in (1, 3, 17, 64, 700):
+        for most in (1, 2, 4, 16, 33, 100, 1000):
+            for tokens in (seqs, seqs * ((most + 1) // 2), seqs * most):
+                for length in (100, 3000, 100000, 1 << 30):
+                    b = _trees(n_seqs=seqs, n_tokens=tokens, table_stride=1 << 27, max_len=length)
+                    n = L.kvc_attend_tree_ws_bytes(d, b, _tree(most=most))
+                    assert n <= 131072 * (4 * head_dim + 8) + 131584
 
 
 def test_binding_refusals():
