@@ -1236,8 +1236,10 @@ class PageLedger:
         self.ws_bytes = int(lib().kvc_resize_ws_bytes(ctypes.byref(desc)))
         self.ws = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=dev)
         self.status = _dev_status(dev)
-        self._args = _LedgerArgs(table.data_ptr(), lens.data_ptr(), self.refs.data_ptr(),
-                                 table.shape[0], table.shape[1])
+
+    def _args(self) -> _LedgerArgs:
+        return _LedgerArgs(self.table.data_ptr(), self.lens.data_ptr(), self.refs.data_ptr(),
+                           self.table.shape[0], self.table.shape[1])
 
     def _rows(self, t: torch.Tensor, what: str) -> int:
         if _int32_tensor(t, 1, what).device != self.device:
@@ -1252,7 +1254,7 @@ def fork_async(ledger: PageLedger, src: torch.Tensor, dst: torch.Tensor, stream=
     s, d = ledger._rows(src, "src"), ledger._rows(dst, "dst")
     if src.shape != dst.shape:
         raise ValueError("src and dst must have the same length")
-    _check(lib().kvc_fork(ledger.desc, ledger._args, s, d, src.shape[0],
+    _check(lib().kvc_fork(ledger.desc, ledger._args(), s, d, src.shape[0],
                           ledger.status.data_ptr(), _paged_stream(stream, ledger.device)),
            "kvc_fork")
 
@@ -1265,7 +1267,7 @@ def resize_async(ledger: PageLedger, pool: torch.Tensor, new_lens: torch.Tensor,
     n = ledger._rows(new_lens, "new_lens")
     if new_lens.shape != ledger.lens.shape:
         raise ValueError("new_lens must have an entry for each row")
-    _check(lib().kvc_resize(ledger.desc, ledger._args, n,
+    _check(lib().kvc_resize(ledger.desc, ledger._args(), n,
                             _pool_ptr(ledger.desc, pool, ledger.device), ledger.ws.data_ptr(),
                             ledger.ws_bytes, ledger.status.data_ptr(),
                             _paged_stream(stream, ledger.device)), "kvc_resize")

@@ -189,6 +189,20 @@ def test_resize_errors():
     assert bool((st.ledger.refs >= 0).all())
 
 
+def test_the_ledgers_tensors_are_read_at_each_call():
+    st = State(4, 4, 16, 12)
+    st.resize([20, 5, 0, 33])
+    st.check()
+    old = [getattr(st.ledger, k) for k in ("table", "lens", "refs")]
+    before = [t.clone() for t in old]
+    for k, t in zip(("table", "lens", "refs"), old):
+        setattr(st.ledger, k, t.clone())
+    st.fork([0], [2])
+    st.resize([21, 40, 22, 0])
+    st.check()
+    assert all(torch.equal(a, b) for a, b in zip(old, before))
+
+
 def test_forked_sequences_decode_apart():
     """A restored context forked three ways: each continuation appends its own
     token and attends; all read the shared pages and none another's token."""
