@@ -883,9 +883,10 @@ __device__ __forceinline__ void attend_part(const AttendArgs &a, uint8_t *lds, c
   const int32_t w_full = kTree ? r_first.base : w_first.hi;
   const int32_t n_tiles = end > begin ? (end - begin + TOK - 1) / TOK : 0;
   constexpr uint32_t kTileShift = TOK == 64 ? 6 : 5;
-  const int32_t t_lo = kTree ? (int32_t)min((uint32_t)n_tiles, part.lo << (a.step_shift - kTileShift))
+  const uint32_t up = a.step_shift - kTileShift;  // of trees: log2 of a step's tiles
+  const int32_t t_lo = kTree ? (int32_t)min((uint32_t)n_tiles, part.lo << up)
                              : (int32_t)((int64_t)n_tiles * part.lo / part.of);
-  const int32_t t_hi = kTree ? (int32_t)min((uint32_t)n_tiles, part.hi << (a.step_shift - kTileShift))
+  const int32_t t_hi = kTree ? (int32_t)min((uint32_t)n_tiles, part.hi << up)
                              : (int32_t)((int64_t)n_tiles * (part.lo + 1) / part.of);
   const uint32_t qh = hk * a.group + row.head;
   const Scale sc_q = scale_of(a.scale);
@@ -1817,7 +1818,8 @@ Plan make_tree_plan(const kvc_paged_desc &p, const kvc_paged_batch &b, uint32_t 
   while (whole ? steps() > 1 : units * steps() >= (1ull << 31)) ++w.shift;
   w.min_steps = whole ? 1 : std::max(1u, (w.rows <= 32 ? 128u : 256u) >> w.shift);
   // pieces of a head's line: waves of k_attend_few, workgroups of k_attend_tree
-  const uint32_t slots = w.rows <= 32 ? resident(p.head_dim) * 4 : resident(p.head_dim) * 128 / w.rows;
+  const uint32_t slots =
+      w.rows <= 32 ? resident(p.head_dim) * 4 : resident(p.head_dim) * 128 / w.rows;
   w.pieces = (uint32_t)std::min<uint64_t>(std::min(512u, std::max(1u, slots / p.n_kv_heads)),
                                           (w.tiles * steps() + w.min_steps - 1) / w.min_steps);
   const uint32_t grid = w.pieces * p.n_kv_heads;

@@ -317,7 +317,8 @@ __global__ __launch_bounds__(1024) void k_resize(LedgerArgs a, const int32_t *ne
     uint32_t off = (uint32_t)before;  // below 2^31: at most n_pages
     if (need[k] >> 48) {
       const uint32_t e = a.page.div((uint32_t)s_old[r]);
-      plan->copy[before >> 48] = Copy{s_page[r], (int32_t)off, s_old[r] - (int32_t)(e * a.page.d), 0};
+      const int32_t tokens = s_old[r] - (int32_t)(e * a.page.d);
+      plan->copy[before >> 48] = Copy{s_page[r], (int32_t)off, tokens, 0};
       s_page[r] = (int32_t)(before >> 48);
     } else {
       s_page[r] = -1;

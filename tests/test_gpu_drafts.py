@@ -433,7 +433,8 @@ def test_drafts_captured_and_replayed():
         kvc.keep_async(st.desc, st.batch, pool, path, kept, new_lens, st.n_tok, wsp.status)
 
     def buffers():
-        return (st.pool.clone(), torch.zeros_like(st.q), torch.zeros(st.q.shape, dtype=F16, device=DEV),
+        return (st.pool.clone(), torch.zeros_like(st.q),
+                torch.zeros(st.q.shape, dtype=F16, device=DEV),
                 torch.zeros(2, dtype=torch.int32, device=DEV),
                 kvc.PagedWorkspace(st.desc, st.batch, st.n_tok, tree=st.tree))
 

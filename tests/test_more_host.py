@@ -120,7 +120,8 @@ def test_sinks_refusals(L):
     assert _sinks(L, lse=A + 2) == INVALID and _sinks(L, scale=float("nan")) == INVALID
     long = _batch(table_stride=10000, max_len=100000)
     need = L.kvc_attend_ws_bytes(_desc(), long)
-    assert _sinks(L, b=long, ws_bytes=need - 1) == CAPACITY and _sinks(L, b=long, ws=None) == INVALID
+    assert _sinks(L, b=long, ws_bytes=need - 1) == CAPACITY
+    assert _sinks(L, b=long, ws=None) == INVALID
     assert L.kvc_attend_sinks(_desc(), None, 0, A, A, 1024, 1.0, 5, 2, A, 1024, A, A, 1 << 40, A,
                               None) == INVALID
 
