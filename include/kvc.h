@@ -634,9 +634,9 @@ kvc_status kvc_attend_tree(const kvc_paged_desc *p, const kvc_paged_batch *b,
  * path[b][1] < .. (kept[b] of them) move to the places 0, 1, .. of its new
  * tokens, in every layer, and new_lens[b] = lens[b] - n_b + kept[b].  path:
  * device [n_seqs][path_stride], entries from kept[b] on are not read; kept and
- * new_lens: device [n_seqs]; new_lens overlaps none of lens, kept and path
- * (KVC_ERR_SHAPE).  The pages of the new tokens are the sequence's own (after a
- * fork kvc_resize makes them so).
+ * new_lens: device [n_seqs]; new_lens overlaps none of lens, kept, path,
+ * q_start and the table (KVC_ERR_SHAPE).  The pages of the new tokens are the
+ * sequence's own (after a fork kvc_resize makes them so).
  * path_stride is at most 4096, 2 * n_layers * n_kv_heads * head_dim below
  * 2^34 (else KVC_ERR_SHAPE).  A path that does not rise or leaves the tree, or
  * a bad page, stores KVC_ERR_SHAPE; that sequence then stays as it is, with

@@ -433,7 +433,8 @@ kvc_status kvc_keep(const kvc_paged_desc *p, const kvc_paged_batch *b, void *poo
     return new_lens < p + n && p < new_lens + b->n_seqs;
   };
   if (overlaps(b->lens, b->n_seqs) || overlaps(kept, b->n_seqs) ||
-      overlaps(path, (uint64_t)b->n_seqs * path_stride))
+      overlaps(path, (uint64_t)b->n_seqs * path_stride) || overlaps(b->q_start, b->n_seqs + 1ull) ||
+      overlaps(b->table, (uint64_t)b->n_seqs * b->table_stride))
     return KVC_ERR_SHAPE;
   KeepArgs a;
   a.s = to_seqs(p, b);

@@ -161,6 +161,10 @@ def test_keep_refusals(L):
         assert _keep(L, new_lens=at, kept=4 * A, path=5 * A) == SHAPE
         assert _keep(L, b=_trees(lens=3 * A), new_lens=at, path=5 * A) == SHAPE
         assert _keep(L, b=_trees(lens=3 * A), new_lens=at, kept=4 * A) == SHAPE
+    # q_start: 4 entries at 6 A; the table: 3 * 10 at 7 A
+    apart = dict(lens=3 * A, q_start=6 * A, table=7 * A, table_stride=10)
+    for at in (6 * A - 8, 6 * A + 12, 7 * A - 8, 7 * A + 116):
+        assert _keep(L, b=_trees(**apart), new_lens=at, kept=4 * A, path=5 * A) == SHAPE
     # the last of path's 3 * 4 entries
     assert _keep(L, b=_trees(lens=3 * A), new_lens=A + 44, kept=4 * A) == SHAPE
     wide = _desc(n_layers=32767, n_heads=4096, n_kv_heads=4096, head_dim=256, page_tokens=1)
