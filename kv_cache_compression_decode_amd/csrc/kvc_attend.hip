@@ -1725,7 +1725,10 @@ __global__ __launch_bounds__(D * 2) void k_attend_tree_join(AttendArgs a) {
     acc *= alpha;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      if (pm[j] == ninf()) continue;  // a part in which the row sees nothing
+      if (i0 + j * S >= parts) continue;
+      // A part in which the row sees nothing adds zeros; so does one whose scores
+      // are all minus infinity.  Its maximum is that of one whose scores are all
+      // NaN, too, which must come through: no part is left out by its maximum.
       const float f = __builtin_amdgcn_exp2f(pm[j] - ref);
       l = __builtin_fmaf(pl[j], f, l);
 #pragma unroll
@@ -1741,9 +1744,9 @@ __global__ __launch_bounds__(D * 2) void k_attend_tree_join(AttendArgs a) {
 #pragma unroll
     for (uint32_t i = 1; i < S; ++i) mm = __builtin_fmaxf(mm, s_m[i]);
     const float f = __builtin_amdgcn_exp2f(m - (mm == ninf() ? 0.0f : mm));
-    if (lane == 0) s_l[stream] = m == ninf() ? 0.0f : l * f;
+    if (lane == 0) s_l[stream] = l * f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s_acc[stream][lane * 4 + e] = m == ninf() ? 0.0f : acc[e] * f;
+    for (int e = 0; e < 4; ++e) s_acc[stream][lane * 4 + e] = acc[e] * f;
     __syncthreads();
     if (g != 0) return;
     m = mm;
