@@ -951,9 +951,20 @@ class Tree:
                          self.max_tokens, 0)
 
     def _check(self, n: int, device) -> None:
-        if self.parent.shape[0] != n or self.parent.device != device:
+        """At each call, since the fields may be replaced."""
+        if not 1 <= self.max_tokens <= 4096:
+            raise ValueError("max_tokens must be between 1 and 4096")
+        parent = _int32_tensor(self.parent, 1, "parent")
+        depth = _int32_tensor(self.depth, 1, "depth")
+        m = self.mask
+        if not m.is_cuda or m.dtype != torch.int64 or not m.is_contiguous():
+            raise ValueError("mask must be a contiguous int64 CUDA tensor")
+        if (parent.shape[0] != n or parent.device != device or depth.device != device
+                or m.device != device):
             raise ValueError("the tree must have an entry for each new token, on the batch's "
                              "device")
+        if depth.shape[0] != n or m.shape != (n, (self.max_tokens + 63) // 64):
+            raise ValueError("mask must be [n_tokens][(max_tokens + 63) / 64], depth [n_tokens]")
 
 
 class PagedWorkspace:
@@ -1016,8 +1027,15 @@ class HeadNorm:
             raise ValueError("the norms' weights must have one shape and device")
         self.q_weight, self.k_weight, self.eps = q_weight, k_weight, float(eps)
 
-    def _args(self) -> _HeadNormArgs:
-        return _HeadNormArgs(self.q_weight.data_ptr(), self.k_weight.data_ptr(), self.eps, 0)
+    def _args(self, dim: int, device) -> _HeadNormArgs:
+        q, k = self.q_weight, self.k_weight  # at each call: they may have been replaced
+        f32 = torch.float32
+        if (q.shape != (dim,) or k.shape != (dim,) or q.dtype is not f32 or k.dtype is not f32
+                or q.device != device or k.device != device or not q.is_contiguous()
+                or not k.is_contiguous()):
+            raise ValueError("the norms' weights must be contiguous float32 tensors of head_dim "
+                             "entries, on the batch's device")
+        return _HeadNormArgs(q.data_ptr(), k.data_ptr(), self.eps, 0)
 
 
 def _cache_type(desc: PagedDesc, t: torch.Tensor, what: str) -> None:
@@ -1096,8 +1114,7 @@ def append_async(desc: PagedDesc, batch: PagedBatch, layer: int, pool: torch.Ten
                                 None if rope is None else rope._args(), wsp.status.data_ptr(),
                                 _paged_stream(stream, dev)), "kvc_append")
         return
-    if norm is not None and (norm.k_weight.shape[0] != dim or norm.k_weight.device != dev):
-        raise ValueError("the norms' weights must have head_dim entries, on the batch's device")
+    norm_args = None if norm is None else norm._args(dim, dev)
     if tree is not None:
         tree._check(n, dev)
         if batch.q_start is None:
@@ -1107,7 +1124,7 @@ def append_async(desc: PagedDesc, batch: PagedBatch, layer: int, pool: torch.Ten
                                  None if q is None else q.data_ptr(), qs,
                                  None if q is None else q_out.data_ptr(), os_,
                                  None if rope is None else rope._args(),
-                                 None if norm is None else norm._args(),
+                                 norm_args,
                                  None if tree is None else tree.depth.data_ptr(),
                                  wsp.status.data_ptr(), _paged_stream(stream, dev)),
            "kvc_append_norm")
@@ -1139,12 +1156,13 @@ def _attend(name: str, desc: PagedDesc, batch: PagedBatch, layer: int, pool, q, 
     _u32(sinks, "sinks")
     _u32(layer, "layer")
     _workspace_check(wsp, dev)
+    if tree is not None:
+        tree._check(n, dev)
     head = (layer, _pool_ptr(desc, pool, dev), q.data_ptr(), qs,
             dim ** -0.5 if scale is None else scale)
     tail = (out.data_ptr(), os_, None if lse is None else lse.data_ptr(), wsp.ws.data_ptr(),
             wsp.ws_bytes, wsp.status.data_ptr(), _paged_stream(stream, dev))
     if tree is not None:
-        tree._check(n, dev)
         code = lib().kvc_attend_tree(desc, batch._args(desc, n), tree._args(), *head, *tail)
     elif sinks:
         if (name == "kvc_attend") != (batch.q_start is None):
@@ -1218,28 +1236,36 @@ class PageLedger:
     lens [rows] tokens each, and how many rows hold each page: refs [n_pages]
     (default: no page is held, all lens are 0).  table and lens may be a
     PagedBatch's.  fork_async and resize_async keep the three in line; device
-    errors stay in status.  One call at a time: the ledger has their workspace."""
+    errors stay in status.  One call at a time: the ledger has their workspace.
+    The tensors may be replaced between calls, by such of the same device that
+    fit each other."""
 
     def __init__(self, desc: PagedDesc, table: torch.Tensor, lens: torch.Tensor,
                  refs: Optional[torch.Tensor] = None):
         dev = table.device
         self.desc, self.device = desc, dev
-        self.table = _int32_tensor(table, 2, "table")
-        self.lens = _int32_tensor(lens, 1, "lens")
         if refs is None:
             refs = torch.zeros(desc.n_pages, dtype=torch.int32, device=dev)
+        self.table = _int32_tensor(table, 2, "table")
+        self.lens = _int32_tensor(lens, 1, "lens")
         self.refs = _int32_tensor(refs, 1, "refs")
-        if lens.shape[0] != table.shape[0] or refs.shape[0] != desc.n_pages:
-            raise ValueError("lens must have an entry for each row, refs one for each page")
-        if lens.device != dev or refs.device != dev:
-            raise ValueError("the ledger's tensors must be on one device")
+        self._args()
         self.ws_bytes = int(lib().kvc_resize_ws_bytes(ctypes.byref(desc)))
         self.ws = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=dev)
         self.status = _dev_status(dev)
 
     def _args(self) -> _LedgerArgs:
-        return _LedgerArgs(self.table.data_ptr(), self.lens.data_ptr(), self.refs.data_ptr(),
-                           self.table.shape[0], self.table.shape[1])
+        # at each call: the tensors may have been replaced
+        table, lens, refs = self.table, self.lens, self.refs
+        i32, dev, shape = torch.int32, self.device, table.shape
+        if (table.dtype is not i32 or lens.dtype is not i32 or refs.dtype is not i32
+                or table.device != dev or lens.device != dev or refs.device != dev
+                or len(shape) != 2 or not table.is_contiguous() or not lens.is_contiguous()
+                or not refs.is_contiguous()):
+            raise ValueError("the ledger's tensors must be contiguous int32 tensors on its device")
+        if lens.shape != shape[:1] or refs.shape != (self.desc.n_pages,):
+            raise ValueError("lens must have an entry for each row, refs one for each page")
+        return _LedgerArgs(table.data_ptr(), lens.data_ptr(), refs.data_ptr(), *shape)
 
     def _rows(self, t: torch.Tensor, what: str) -> int:
         if _int32_tensor(t, 1, what).device != self.device:
