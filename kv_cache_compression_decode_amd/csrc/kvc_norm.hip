@@ -62,7 +62,7 @@ __global__ __launch_bounds__(256) void k_append_norm(NormArgs a) {
   const int64_t at = a.depth ? (int64_t)base + a.depth[row] : pos;  // the rotation's position
   uint32_t slot;
   if (!a.s.slot_of(a.s.table + (uint64_t)b * a.s.table_stride, (uint32_t)pos, slot) ||
-      (a.rotary && (at < 0 || at >= a.n_positions))) {
+      at < 0 || (a.rotary && at >= a.n_positions)) {
     if (first) set_status(a.status, KVC_ERR_SHAPE);
     return;
   }
