@@ -670,7 +670,8 @@ typedef struct {
  * out.  Forks whose rows are outside the table or get in each other's way (a
  * dst that stands twice, or is a src too) are left out and store
  * KVC_ERR_SHAPE, as are rows with a bad length; so does a page id outside the
- * pool or the release of a free page, which is passed over.
+ * pool or the release of a free page, which is passed over.  src and dst
+ * overlap none of the ledger's arrays (KVC_ERR_SHAPE).
  */
 kvc_status kvc_fork(const kvc_paged_desc *p, const kvc_ledger *g, const int32_t *src,
                     const int32_t *dst, uint32_t n, int32_t *dev_status, hipStream_t stream);
@@ -687,8 +688,9 @@ uint64_t kvc_resize_ws_bytes(const kvc_paged_desc *p);
  * for each entry that it newly reaches.  Free pages are taken lowest id first.
  * If they do not suffice, no row grows: KVC_ERR_CAPACITY on the device.  A row
  * whose lengths are negative or above table_stride * page_tokens stays as it
- * is: KVC_ERR_SHAPE, as for bad pages (see kvc_fork).  ws: kvc_resize_ws_bytes
- * bytes, 256-byte aligned, one call at a time.
+ * is: KVC_ERR_SHAPE, as for bad pages (see kvc_fork).  new_lens overlaps none
+ * of the ledger's arrays (KVC_ERR_SHAPE).  ws: kvc_resize_ws_bytes bytes,
+ * 256-byte aligned, one call at a time.
  */
 kvc_status kvc_resize(const kvc_paged_desc *p, const kvc_ledger *g, const int32_t *new_lens,
                       void *pool, void *ws, uint64_t ws_bytes, int32_t *dev_status,

@@ -1289,7 +1289,7 @@ def resize_async(ledger: PageLedger, pool: torch.Tensor, new_lens: torch.Tensor,
                  stream=None) -> None:
     """Launch kvc_resize: every row shrinks or grows to new_lens [rows] tokens
     (0 frees it).  A row that grows out of a page that others hold too gets a
-    copy of its own (no sync)."""
+    copy of its own (no sync).  new_lens is not the ledger's lens."""
     n = ledger._rows(new_lens, "new_lens")
     if new_lens.shape != ledger.lens.shape:
         raise ValueError("new_lens must have an entry for each row")

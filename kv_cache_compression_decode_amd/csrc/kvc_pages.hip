@@ -9,6 +9,11 @@ namespace {
 
 uint64_t row_bytes(const kvc_paged_desc *p) { return (uint64_t)p->n_kv_heads * p->head_dim * 2; }
 
+// Do n entries at p and m at q share one?
+bool overlap(const int32_t *p, uint64_t n, const int32_t *q, uint64_t m) {
+  return p < q + m && q < p + n;
+}
+
 // -------------------------------------------------------------------- keep
 // Token rows base + path[i] go to base + i, in every layer's keys and values.
 // The path rises, so path[i] >= i: a thread that owns 16 bytes of the rows of
@@ -395,6 +400,12 @@ kvc_status ledger_check(const kvc_paged_desc *p, const kvc_ledger *g) {
   return KVC_OK;
 }
 
+// n entries at p, which a call reads, over what it writes
+bool over_ledger(const kvc_paged_desc *p, const kvc_ledger *g, const int32_t *in, uint64_t n) {
+  return overlap(in, n, g->table, (uint64_t)g->n_rows * g->table_stride) ||
+         overlap(in, n, g->lens, g->n_rows) || overlap(in, n, g->refs, p->n_pages);
+}
+
 LedgerArgs to_ledger(const kvc_paged_desc *p, const kvc_ledger *g, int32_t *status) {
   LedgerArgs a;
   a.table = g->table;
@@ -431,12 +442,12 @@ kvc_status kvc_keep(const kvc_paged_desc *p, const kvc_paged_batch *b, void *poo
   if (!kept || !aligned(kept, 4) || !new_lens || !aligned(new_lens, 4)) return KVC_ERR_INVALID_ARG;
   if (path_stride && (!path || !aligned(path, 4))) return KVC_ERR_INVALID_ARG;
   // workgroups read these while others write new_lens
-  const auto overlaps = [&](const int32_t *p, uint64_t n) {
-    return new_lens < p + n && p < new_lens + b->n_seqs;
+  const auto over = [&](const int32_t *p, uint64_t n) {
+    return overlap(new_lens, b->n_seqs, p, n);
   };
-  if (overlaps(b->lens, b->n_seqs) || overlaps(kept, b->n_seqs) ||
-      overlaps(path, (uint64_t)b->n_seqs * path_stride) || overlaps(b->q_start, b->n_seqs + 1ull) ||
-      overlaps(b->table, (uint64_t)b->n_seqs * b->table_stride))
+  if (over(b->lens, b->n_seqs) || over(kept, b->n_seqs) ||
+      over(path, (uint64_t)b->n_seqs * path_stride) || over(b->q_start, b->n_seqs + 1ull) ||
+      over(b->table, (uint64_t)b->n_seqs * b->table_stride))
     return KVC_ERR_SHAPE;
   KeepArgs a;
   a.s = to_seqs(p, b);
@@ -465,6 +476,8 @@ kvc_status kvc_fork(const kvc_paged_desc *p, const kvc_ledger *g, const int32_t 
   if (n > kRows) return KVC_ERR_SHAPE;
   if (n == 0) return KVC_OK;
   if (!src || !aligned(src, 4) || !dst || !aligned(dst, 4)) return KVC_ERR_INVALID_ARG;
+  // workgroups read the lists while others write the ledger
+  if (g->n_rows && (over_ledger(p, g, src, n) || over_ledger(p, g, dst, n))) return KVC_ERR_SHAPE;
   hipLaunchKernelGGL(k_fork, dim3(n), dim3(256), 0, stream, to_ledger(p, g, dev_status), src, dst,
                      n);
   return hipGetLastError() == hipSuccess ? KVC_OK : KVC_ERR_HIP;
@@ -484,6 +497,8 @@ kvc_status kvc_resize(const kvc_paged_desc *p, const kvc_ledger *g, const int32_
   if (g->n_rows == 0) return KVC_OK;
   if (!new_lens || !aligned(new_lens, 4) || !ws || !aligned(ws, 256)) return KVC_ERR_INVALID_ARG;
   if (ws_bytes < kvc_resize_ws_bytes(p)) return KVC_ERR_CAPACITY;
+  // (lengths put into the ledger itself would not be seen to change)
+  if (over_ledger(p, g, new_lens, g->n_rows)) return KVC_ERR_SHAPE;
   ResizePlan *plan = static_cast<ResizePlan *>(ws);
   int32_t *found = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + found_at());
   hipLaunchKernelGGL(k_resize, dim3(1), dim3(1024), 0, stream, to_ledger(p, g, dev_status),
