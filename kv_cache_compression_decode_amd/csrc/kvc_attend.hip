@@ -1141,33 +1141,44 @@ __device__ __forceinline__ void attend_part(const AttendArgs &a, uint8_t *lds, c
   if (late && pending) values(s_val + next_odd_of(next_odd_of(odd_at)) * kValBuf<D>);
   if (__ballot(bad) && lane == 0) set_status(a.status, KVC_ERR_SHAPE);
   l += other_half(l);
-  if (!live) return;
+  // A tree's workgroup may go on to another part: there, lanes without a row
+  // compute as the others do and leave out the stores alone.  With nothing but
+  // stores in the branches that only some lanes take, no value that goes on has
+  // to change its register inside one.
+  if (!kTree && !live) return;
   if (part.all) {
     const bool some = row.hi > row.lo;
     const float inv = some ? 1.0f / l : 0.0f;
     TI *op = static_cast<TI *>(a.out) + (uint64_t)row.token * a.out_stride + (uint64_t)qh * D +
              hi * 4;
+    u32x2 w[DT][4];
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        u32x2 w;
-        w[0] = some ? pack2<TI>(o[d][4 * i] * inv, o[d][4 * i + 1] * inv) : 0u;
-        w[1] = some ? pack2<TI>(o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv) : 0u;
-        *reinterpret_cast<u32x2 *>(op + d * 32 + i * 8) = w;
+        w[d][i][0] = some ? pack2<TI>(o[d][4 * i] * inv, o[d][4 * i + 1] * inv) : 0u;
+        w[d][i][1] = some ? pack2<TI>(o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv) : 0u;
       }
-    if (hi == 0 && a.lse)
+    if (live) {
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x2 *>(op + d * 32 + i * 8) = w[d][i];
+    }
+    if (live && hi == 0 && a.lse)
       a.lse[(uint64_t)row.token * a.n_heads + qh] =
           some ? (ref - kShiftBig<TC> + __builtin_amdgcn_logf(l)) * kLn2 : ninf();
   } else {
     float *op = a.part + (part.at * kRows + w0 + n32) * D + hi * 4;
+    if (live) {
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
+      for (int d = 0; d < DT; ++d)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<f32x4 *>(op + d * 32 + i * 8) =
-            f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
-    if (hi == 0) {
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<f32x4 *>(op + d * 32 + i * 8) =
+              f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+    }
+    if (live && hi == 0) {
       a.part_ml[part.at * (2 * kRows) + w0 + n32] = ref;
       a.part_ml[part.at * (2 * kRows) + kRows + w0 + n32] = l;
     }
@@ -1624,7 +1635,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_few(AttendArgs
     for (int r = 0; r < R; ++r) {
       l[r] += __shfl_xor(l[r], 16);
       l[r] += __shfl_xor(l[r], 32);
-      if (!live[r]) continue;
+      // (every lane computes; those without a row leave out the stores alone)
       // a lane's 4 E values are dimensions g4 * 4 E on of its row
       const bool some = row[r].hi > row[r].lo;
       const float f = all ? (some ? 1.0f / l[r] : 0.0f) : 1.0f;
@@ -1637,24 +1648,28 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attend_few(AttendArgs
       if (all) {
         TI *out = static_cast<TI *>(a.out) + (uint64_t)row[r].token * a.out_stride +
                   (uint64_t)h * D + g4 * 4 * E;
+        u32x4 wv[E / 2];
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-          u32x4 wv;
+        for (int i = 0; i < E / 2; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            wv[e] = some ? pack2<TI>(val[8 * i + 2 * e], val[8 * i + 2 * e + 1]) : 0u;
-          store16(out + 8 * i, wv);
+            wv[i][e] = some ? pack2<TI>(val[8 * i + 2 * e], val[8 * i + 2 * e + 1]) : 0u;
+        if (live[r]) {
+#pragma unroll
+          for (int i = 0; i < E / 2; ++i) store16(out + 8 * i, wv[i]);
         }
-        if (g4 == 0 && a.lse)
+        if (live[r] && g4 == 0 && a.lse)
           a.lse[(uint64_t)row[r].token * a.n_heads + h] =
               some ? (m[r] - kShiftBig<TC> + __builtin_amdgcn_logf(l[r])) * kLn2 : ninf();
       } else {
         float *op = a.part + (part * kRows + r * 16 + n16) * D + g4 * 4 * E;
+        if (live[r]) {
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-          *reinterpret_cast<f32x4 *>(op + 4 * i) =
-              f32x4{val[4 * i], val[4 * i + 1], val[4 * i + 2], val[4 * i + 3]};
-        if (g4 == 0) {
+          for (int i = 0; i < E; ++i)
+            *reinterpret_cast<f32x4 *>(op + 4 * i) =
+                f32x4{val[4 * i], val[4 * i + 1], val[4 * i + 2], val[4 * i + 3]};
+        }
+        if (live[r] && g4 == 0) {
           a.part_ml[part * (2 * kRows) + r * 16 + n16] = m[r];
           a.part_ml[part * (2 * kRows) + kRows + r * 16 + n16] = l[r];
         }
