@@ -124,6 +124,11 @@ __global__ __launch_bounds__(256) void k_fork(LedgerArgs a, const int32_t *src, 
   const int32_t s = src[i], d = dst[i];
   if (s < 0) return;  // left out by the caller
   bool bad = s >= (int32_t)a.n_rows || d < 0 || d >= (int32_t)a.n_rows;
+  bool clash = false;
+  for (uint32_t j = threadIdx.x; j < n; j += 256) {
+    const int32_t sj = src[j], dj = dst[j];
+    clash = clash || (sj >= 0 && (sj == d || dj == s || (j != i && dj == d)));
+  }
   // Both lengths are read, and looked at, before the barrier: thread 0 stores
   // the new one when its own wave is done, while others may still be at work.
   int32_t from = 0, held = 0;
@@ -132,11 +137,7 @@ __global__ __launch_bounds__(256) void k_fork(LedgerArgs a, const int32_t *src, 
     held = a.lens[d];
     bad = !a.len_ok(from) || !a.len_ok(held);
   }
-  for (uint32_t j = threadIdx.x; j < n; j += 256) {
-    const int32_t sj = src[j], dj = dst[j];
-    bad = bad || (sj >= 0 && (sj == d || dj == s || (j != i && dj == d)));
-  }
-  bad = __syncthreads_or(bad);
+  bad = __syncthreads_or(bad || clash);
   if (bad) {
     if (threadIdx.x == 0) set_status(a.status, KVC_ERR_SHAPE);
     return;
