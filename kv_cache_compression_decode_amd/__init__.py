@@ -935,7 +935,8 @@ class Tree:
     before it, or -1 if it follows the cached context.  max_tokens bounds the
     new tokens of a sequence.  tree_async fills mask [n_tokens][words] (which
     of them each one sees: itself and what it follows) and depth [n_tokens];
-    once for every step and layer with trees of this shape."""
+    once for every step and layer with trees of this shape.  The tensors may be
+    replaced between calls, by such that fit."""
 
     def __init__(self, parent: torch.Tensor, max_tokens: int):
         self.parent = _int32_tensor(parent, 1, "parent")

@@ -1266,8 +1266,8 @@ __global__ __launch_bounds__(256) void k_attend_tile_join(AttendArgs a) {
 // is asked for.
 //
 // 15 trees of 17 to 60 tokens over 1,500 to 16,000, 8 heads to each of 8 KV heads
-// (156 GFLOP): 264 us (331 in equal splits of whole sequences; 300 with 128-row
-// tiles).  The matrix units are busy 27% of it and the vector units as much;
+// (156 GFLOP): 258 to 264 us (331 in equal splits of whole sequences; 300 with
+// 128-row tiles).  The matrix units are busy 27% of it and the vector units as much;
 // 27% of the tiles' rows are empty.  Steps weighted by their tile's waves moved
 // the cuts but gained nothing.
 
@@ -1819,7 +1819,11 @@ Plan make_tree_plan(const kvc_paged_desc &p, const kvc_paged_batch &b, uint32_t 
   w.wg_heads = 1;
   const uint32_t group = p.n_heads / p.n_kv_heads;
   const uint64_t most = (uint64_t)max_new * group, avg = (uint64_t)b.n_tokens * group / b.n_seqs;
-  // (32 rows of 256 dimensions would not fit the registers)
+  // 32 rows of 256 dimensions do not fit the registers.  The lower tiles are for
+  // sequences that fill one of them on average: 8 heads to each of 8 KV heads, 16
+  // sequences of 8,000, 128 rows each take 132 us in tiles of 128 and 147 in tiles
+  // of 256, 136 rows 168 and 158, 384 rows 355 and 284; 48 sequences of 3,000: 128
+  // rows 169 and 176, 136 rows 257 and 189.
   w.rows = most <= 16                         ? 16
            : most <= 32 && p.head_dim != 256  ? 32
            : avg <= 128 || p.head_dim == 256  ? 128

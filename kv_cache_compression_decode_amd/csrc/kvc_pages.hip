@@ -116,7 +116,7 @@ struct LedgerArgs {
 // source's page ids are copied and counted.  Counts are sums, so their order
 // does not show.  Forks that get in each other's way (a destination twice, or
 // a source too) would depend on it: every workgroup looks through the list for
-// such and leaves them out.  It is a chain of five dependent accesses: 3.2 us for
+// such and leaves them out.  It is a chain of five dependent accesses: 3.1 us for
 // 4 forks, 4.8 for 64.
 __global__ __launch_bounds__(256) void k_fork(LedgerArgs a, const int32_t *src, const int32_t *dst,
                                               uint32_t n) {
@@ -165,9 +165,10 @@ __global__ __launch_bounds__(256) void k_fork(LedgerArgs a, const int32_t *src, 
 // a shared, partly filled page are noted, and the pages needed are found among
 // the counts, lowest first, and handed out row by row.  The counts' scan reads
 // 4 n_pages bytes at most (16,384 counts at a time) and ends when enough are
-// found.  It is latency: 8.4 us for 5 rows, 11.7 for 80 (18.4 and 21.8 with
-// fences for other workgroups, which there are none of, and the found pages
-// passed through memory).  A second launch copies the shared pages' tokens:
+// found.  It is latency: 8.4 to 9.4 us for 5 rows, 11.7 to 14 for 80 (18.4 and 21.8
+// with fences for other workgroups, which there are none of, and the found pages
+// passed through memory).  Where the free pages lie behind 100,000 held ones the
+// scan takes 28 us, behind 1,000,000 it takes 318.  A second launch copies the shared pages' tokens:
 // each byte once in and once out, 64 pages of 64 tokens in 32 layers of 8 x 128
 // (384 MB) in 47 us, which is more than HBM gives a copy (4.8 TB/s): the last-level
 // cache holds part of it.
